@@ -67,7 +67,8 @@ typedef enum {
 
 typedef enum {
     ORTHRUS_BF16 = 0,
-    ORTHRUS_F32 = 1
+    ORTHRUS_F32 = 1,
+    ORTHRUS_F16 = 2 /* the layer operators at the end of this header only */
 } orthrus_dtype;
 
 #define ORTHRUS_OK 0
@@ -81,6 +82,7 @@ typedef enum {
 #define ORTHRUS_STATUS_CAPACITY 0x1   /* ctx_lens[b] < 0 or ctx_lens[b] + K > S_max */
 #define ORTHRUS_STATUS_ACCEPT 0x2     /* accepted_len[b] outside [0, K]             */
 #define ORTHRUS_STATUS_TIMEOUT 0x4    /* an on-chip pipeline wait gave up          */
+#define ORTHRUS_STATUS_PAGE 0x8       /* a block-table entry outside [0, num_pages) */
 
 /* Largest supported sizes (checked on the host). */
 #define ORTHRUS_MAX_HEAD_DIM 256
@@ -447,6 +449,209 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
                                     int hidden, int Hq, int Hkv, int D, int S_max, void *q_out,
                                     void *k_cache, void *v_cache, void *workspace,
                                     size_t workspace_bytes, int32_t *status, void *stream);
+
+/* ==========================================================================
+ * Layer operators around the decode step's attention: what a whole layer of
+ * the frozen AR model runs between the calls above (norm, 8-bit projections,
+ * rotary positions) and its one-token-at-a-time decoding over a paged cache.
+ * (The pages describe none of them; they are the standard operators of the
+ * models the method is applied to.)  The conventions at the top hold, with two
+ * additions: these calls also take ORTHRUS_F16, and where a stride is an
+ * argument it counts elements and the innermost dimension is contiguous.
+ * ========================================================================== */
+
+#define ORTHRUS_FP8_BLOCK 128          /* values that share one scale */
+#define ORTHRUS_MAX_NORM_WIDTH 32768   /* H of orthrus_rmsnorm        */
+
+/*
+ * orthrus_rmsnorm — RMS norm of T rows, with the residual's addition before it
+ * and an 8-bit output with scales behind it:
+ *     s = x + residual                       (fp32; s = x without a residual)
+ *     y = s * rsqrt(mean_h(s^2) + eps) * weight
+ * The norm reads s before any rounding; every output is rounded once.
+ *
+ *   x         [T, H] of dtype, rows x_stride elements apart.
+ *   residual  optional [T, H], dense.  sum_out [T, H], dense, receives s; it is
+ *             required with a residual and must be NULL without one.  It may
+ *             be the residual itself, or x where x is dense.
+ *   weight    [H] of dtype.
+ *   out       optional [T, H] of dtype, dense: y.  May be x where x is dense.
+ *   out_fp8   optional [T, H] e4m3, dense, with out_scale [T, ceil(H / 128)]
+ *             fp32: for each group of 128 columns (the last may be short)
+ *                 scale = max(max|y| / 448, 2^-126),  value = e4m3(y / scale)
+ *             (nearest even), so value * scale stands for y and a group of
+ *             zeros has a finite scale.  A NaN stays a NaN and does not enter
+ *             the maximum.
+ *             At least one of out and out_fp8 is given.
+ * Supported: H <= ORTHRUS_MAX_NORM_WIDTH, any T.  16-byte aligned pointers,
+ * x_stride and H multiples of 8 take the vector path; anything else is read
+ * element by element.
+ */
+ORTHRUS_API int orthrus_rmsnorm(orthrus_dtype dtype, const void *x, int64_t x_stride,
+                                const void *residual, const void *weight, int T, int H, float eps,
+                                void *sum_out, void *out, void *out_fp8, float *out_scale,
+                                void *stream);
+
+/*
+ * orthrus_quantize_fp8 — x [T, H] of dtype (rows x_stride apart) to e4m3 with a
+ * scale per row and group of 128 columns, as out_fp8 / out_scale above with y =
+ * x: the inputs of 8-bit products that no norm produces (attention output,
+ * gated activations).  Any H.
+ */
+ORTHRUS_API int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t x_stride, int T,
+                                     int H, void *out_fp8, float *out_scale, void *stream);
+
+/*
+ * orthrus_fp8_matmul — matrix product in 8-bit floating point with a scale for
+ * each block of 128:
+ *     out[m, n] = sum_kb a_scale[m, kb] * w_scale[n / 128, kb] *
+ *                 sum_{k in block kb} a[m, k] * w[n, k]
+ * fp32 throughout (the products of a block are summed on the tensor cores,
+ * each block's sum is scaled and added in fp32), rounded once to out_dtype.
+ *
+ *   a        [M, K] e4m3, dense;  a_scale [M, ceil(K / 128)] fp32.
+ *   w        [N, K] e4m3, dense;  w_scale [ceil(N / 128), ceil(K / 128)] fp32
+ *            (one scale per 128 x 128 block; short blocks at the ends).
+ *   out      [M, N] of out_dtype, dense.
+ *   status   optional device int32 (ORTHRUS_STATUS_TIMEOUT only).
+ * Supported: any M and N, K a multiple of 16; a and w 16-byte aligned (their
+ * rows are then too), out aligned to its element; sm_100 devices only.  No
+ * workspace: results do not depend on scheduling and calls may overlap.
+ */
+ORTHRUS_API int orthrus_fp8_matmul(const void *a, const float *a_scale, const void *w,
+                                   const float *w_scale, int M, int N, int K,
+                                   orthrus_dtype out_dtype, void *out, int32_t *status,
+                                   void *stream);
+
+typedef enum {
+    ORTHRUS_ROPE_HALF = 0,       /* pair i = (x[i], x[i + rot/2])   */
+    ORTHRUS_ROPE_INTERLEAVED = 1 /* pair i = (x[2i], x[2i + 1])     */
+} orthrus_rope_layout;
+
+typedef enum {
+    ORTHRUS_ROPE_PLAIN = 0,
+    ORTHRUS_ROPE_LINEAR = 1,     /* every frequency divided by factor             */
+    ORTHRUS_ROPE_NTK = 2,        /* theta * factor^(rot / (rot - 2))              */
+    ORTHRUS_ROPE_YARN = 3        /* by bands: arXiv 2309.00071, sections 3.2, 3.4 */
+} orthrus_rope_scaling;
+
+/*
+ * orthrus_rope_table — the frequencies of a rotary embedding, computed on the
+ * HOST (no device needed): turns[i] = f_i / (2 pi) for the rot_dim / 2 pairs,
+ * f_i = theta^(-2 i / rot_dim) before scaling, and the factor on the rotated
+ * values (*magnitude: 1, or 0.1 ln(factor) + 1 for ORTHRUS_ROPE_YARN with
+ * factor > 1).  YARN keeps frequencies that turn more than beta_fast times in
+ * orig_len positions, divides those that turn less than beta_slow times by
+ * factor, and blends linearly over the pair index between.  factor is read for
+ * kinds other than PLAIN, orig_len and the betas for YARN.  Upload turns once
+ * and keep it: the calls below read it from the device.
+ */
+ORTHRUS_API int orthrus_rope_table(orthrus_rope_scaling kind, int rot_dim, double theta,
+                                   double factor, double orig_len, double beta_fast,
+                                   double beta_slow, double *turns, float *magnitude);
+
+/*
+ * orthrus_rope — rotary positions of T tokens' queries and keys, with an
+ * optional RMS norm of each head before the rotation:
+ *     x <- x * rsqrt(mean_d(x^2) + eps) * norm_weight          (if given)
+ *     (a, b) <- magnitude * (a cos t - b sin t, b cos t + a sin t)
+ * with t = 2 pi * frac(positions[t] * turns[i]) for pair i of the first rot_dim
+ * elements; the rest of the head is only normed.  The angle's product and
+ * fraction are taken in fp64, so far positions lose nothing; all else is fp32,
+ * rounded once.
+ *
+ *   q, q_out  [T, Hq, D] of dtype; k, k_out [T, Hkv, D], or all of k NULL with
+ *             Hkv = 0.  Outputs may be the inputs themselves (same strides).
+ *   strides   HOST array {q token, q head, q_out token, q_out head, k token,
+ *             k head, k_out token, k_out head}, or NULL for dense tensors.
+ *   positions [T] int32.
+ *   turns     [rot_dim / 2] fp64 (device), magnitude: from orthrus_rope_table.
+ *   q_norm, k_norm  optional [D] of dtype.
+ * Supported: D <= ORTHRUS_MAX_HEAD_DIM, rot_dim even, 0 < rot_dim <= D.  D and
+ * rot_dim multiples of 16, 16-byte aligned pointers and strides that keep that
+ * alignment take the vector path; anything else goes element by element.
+ */
+ORTHRUS_API int orthrus_rope(orthrus_dtype dtype, orthrus_rope_layout layout, const void *q,
+                             void *q_out, const void *k, void *k_out, const int64_t *strides,
+                             const int32_t *positions, const double *turns, float magnitude, int T,
+                             int Hq, int Hkv, int D, int rot_dim, const void *q_norm,
+                             const void *k_norm, float eps, void *stream);
+
+/*
+ * orthrus_rope_append — the same for K new tokens of B sequences at positions
+ * ctx_lens[b] + i, with the rotated keys and the values written into the rows
+ * of a paged cache that these positions name: between the QKV projection and
+ * the attention over that cache.
+ *
+ * A paged cache is a pool k_pages, v_pages [num_pages, Hkv, page_size, D];
+ * position j of sequence b is row j % page_size of page block_table[b, j /
+ * page_size].  The contiguous cache [B, Hkv, S_max, D] of the calls above is
+ * the case num_pages = B, page_size = S_max, max_pages = 1, block_table[b] = b.
+ *
+ *   q, q_out  [B, K, Hq, D]; k, v [B, K, Hkv, D], all of dtype.  Token (b, i)
+ *             is row b * K + i of each tensor's token stride.  With k NULL the
+ *             keys already sit in their rows (orthrus_qkv_project put them
+ *             there): they are rotated in place, v must be NULL and the values
+ *             stay as they are.  q may be NULL with Hq = 0.
+ *   strides   HOST array {q token, q head, q_out token, q_out head, k token,
+ *             k head, v token, v head}, or NULL for dense tensors.
+ *   block_table  [B, max_pages] int32 (device); only the entries of the new
+ *             positions are read.
+ *   ctx_lens  [B] int32, only read (orthrus_kv_commit advances it).  A
+ *             sequence with ctx_lens[b] < 0 or ctx_lens[b] + K > max_pages *
+ *             page_size sets ORTHRUS_STATUS_CAPACITY, a table entry outside
+ *             [0, num_pages) sets ORTHRUS_STATUS_PAGE; the cache rows concerned
+ *             are not touched.  q_out is written in any case.
+ * Two tokens of one call must not name the same row.  Otherwise as
+ * orthrus_rope.
+ */
+ORTHRUS_API int orthrus_rope_append(orthrus_dtype dtype, orthrus_rope_layout layout, const void *q,
+                                    void *q_out, const void *k, const void *v,
+                                    const int64_t *strides, const double *turns, float magnitude,
+                                    int B, int K, int Hq, int Hkv, int D, int rot_dim,
+                                    const void *q_norm, const void *k_norm, float eps,
+                                    void *k_pages, void *v_pages, int num_pages, int page_size,
+                                    const int32_t *block_table, int max_pages,
+                                    const int32_t *ctx_lens, int32_t *status, void *stream);
+
+/*
+ * orthrus_paged_attn — attention of one new token per sequence over a paged
+ * cache (layout: orthrus_rope_append), split over the cache's length and joined
+ * in the same launch: plain AR decoding.
+ *
+ *     out[b, h, :] = sum_j softmax_j(scale * <q[b,h,:], K[b,g,j,:]>) V[b,g,j,:]
+ * over j in [0, ctx_lens[b] + n_new), g = h / (Hq / Hkv).  A sequence with no
+ * visible key gives zeros.
+ *
+ *   dtype     ORTHRUS_BF16 or ORTHRUS_F16, of q, the pages and out.
+ *   q, out    [B, Hq, D], dense.
+ *   n_new     rows past the committed length that are visible: 1 after
+ *             orthrus_rope_append wrote this token's key, 0 where ctx_lens
+ *             already counts it.
+ *   block_table  [B, max_pages] int32; only the entries of visible positions
+ *             are read, and no row past them.  An entry outside [0, num_pages)
+ *             sets ORTHRUS_STATUS_PAGE and its keys are left out; a length
+ *             below zero or above max_pages * page_size sets
+ *             ORTHRUS_STATUS_CAPACITY and that sequence's output is zeros.
+ *   scale     softmax scale; <= 0 selects 1/sqrt(D).
+ *   workspace >= orthrus_paged_attn_workspace_size(B, Hq, Hkv, D) bytes,
+ *             16-byte aligned, zero-filled once before first use; every call
+ *             leaves its counters zero (the rest is scratch).  The size does
+ *             not depend on lengths or pages.  Calls that overlap on the device
+ *             must not share it.
+ * Supported: D 64, 128 or 256; Hq % Hkv == 0; B <= 4096; any page_size.  q, the
+ * pages and the workspace 16-byte aligned.
+ * Numerics: products of 16-bit values are exact in fp32; the softmax weights
+ * enter the second product as two 16-bit terms, the statistics are fp32, the
+ * splits are joined in a fixed order (results do not depend on timing).
+ */
+ORTHRUS_API size_t orthrus_paged_attn_workspace_size(int B, int Hq, int Hkv, int D);
+ORTHRUS_API int orthrus_paged_attn(orthrus_dtype dtype, const void *q, const void *k_pages,
+                                   const void *v_pages, const int32_t *block_table,
+                                   const int32_t *ctx_lens, int n_new, int B, int Hq, int Hkv, int D,
+                                   int num_pages, int page_size, int max_pages, float scale,
+                                   void *out, void *workspace, size_t workspace_bytes,
+                                   int32_t *status, void *stream);
 
 /* Human-readable text for an ORTHRUS_* return code (static storage). */
 ORTHRUS_API const char *orthrus_error_string(int code);

@@ -16,10 +16,12 @@ import torch
 from .build import LIB
 
 DIFF, AR = 0, 1
-BF16, F32 = 0, 1
+BF16, F32, F16 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 
 ERR_ARG, ERR_UNSUPPORTED, ERR_ALIGN, ERR_WORKSPACE, ERR_LAUNCH, ERR_DEVICE = -1, -2, -3, -4, -5, -6
-STATUS_CAPACITY, STATUS_ACCEPT, STATUS_TIMEOUT = 0x1, 0x2, 0x4
+STATUS_CAPACITY, STATUS_ACCEPT, STATUS_TIMEOUT, STATUS_PAGE = 0x1, 0x2, 0x4, 0x8
 
 EXPORTED = ("orthrus_attn_workspace_size", "orthrus_attn", "orthrus_attn_path",
             "orthrus_consensus_workspace_size", "orthrus_consensus",
@@ -28,7 +30,9 @@ EXPORTED = ("orthrus_attn_workspace_size", "orthrus_attn", "orthrus_attn_path",
             "orthrus_lm_head_consensus", "orthrus_rejection_workspace_size",
             "orthrus_rejection_verify", "orthrus_qkv_workspace_size", "orthrus_qkv_project",
             "orthrus_prefill_workspace_size",
-            "orthrus_prefill_attn")
+            "orthrus_prefill_attn", "orthrus_rmsnorm", "orthrus_quantize_fp8", "orthrus_fp8_matmul",
+            "orthrus_rope_table", "orthrus_rope", "orthrus_rope_append",
+            "orthrus_paged_attn_workspace_size", "orthrus_paged_attn")
 
 
 class OrthrusError(RuntimeError):
@@ -87,6 +91,26 @@ def lib():
         L.orthrus_prefill_attn.restype = i32
         L.orthrus_prefill_attn.argtypes = [i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz,
                                            vp, vp]
+        i64, f64 = ctypes.c_int64, ctypes.c_double
+        L.orthrus_rmsnorm.restype = i32
+        L.orthrus_rmsnorm.argtypes = [i32, vp, i64, vp, vp, i32, i32, f32, vp, vp, vp, vp, vp]
+        L.orthrus_quantize_fp8.restype = i32
+        L.orthrus_quantize_fp8.argtypes = [i32, vp, i64, i32, i32, vp, vp, vp]
+        L.orthrus_fp8_matmul.restype = i32
+        L.orthrus_fp8_matmul.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.orthrus_rope_table.restype = i32
+        L.orthrus_rope_table.argtypes = [i32, i32, f64, f64, f64, f64, f64, vp, vp]
+        L.orthrus_rope.restype = i32
+        L.orthrus_rope.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, i32, vp, vp, f32,
+                                   vp]
+        L.orthrus_rope_append.restype = i32
+        L.orthrus_rope_append.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, f32, i32, i32, i32, i32, i32, i32, vp, vp,
+                                          f32, vp, vp, i32, i32, vp, i32, vp, vp, vp]
+        L.orthrus_paged_attn_workspace_size.restype = sz
+        L.orthrus_paged_attn_workspace_size.argtypes = [i32, i32, i32, i32]
+        L.orthrus_paged_attn.restype = i32
+        L.orthrus_paged_attn.argtypes = [i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp,
+                                         sz, vp, vp]
         L.orthrus_error_string.restype = ctypes.c_char_p
         L.orthrus_error_string.argtypes = [i32]
         L.orthrus_version.restype = i32
@@ -303,3 +327,282 @@ def orthrus_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                                     workspace.numel() * workspace.element_size(), _ptr(status),
                                     _stream(stream))
     _check("orthrus_prefill_attn", rc)
+
+
+# ---------------------------------------------------------------- layer operators
+_CODES = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
+
+
+def _code(dt: torch.dtype) -> int:
+    code = _CODES.get(dt)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dt}")
+    return code
+
+
+def _same(tensors, dtype: torch.dtype) -> None:
+    for t in tensors:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"expected {dtype}, got {t.dtype}")
+
+
+def _shape(t: torch.Tensor, *shape) -> None:
+    if t.shape != shape:
+        raise ValueError(f"expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _where(tensors, stream):
+    """The device index all tensors share and the raw stream the call goes to
+    (by default that device's current one)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("liborthrus takes device tensors")
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on devices {dev} and {d}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _launch(name: str, dev: int, *args) -> None:
+    """Call the entry point with the tensors' device current."""
+    fn = getattr(lib(), name)
+    now = torch._C._cuda_getDevice()
+    if now == dev:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc != 0:
+        _check(name, rc)
+
+
+def _dense(*tensors) -> None:
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("liborthrus takes contiguous tensors here")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(x: torch.Tensor):
+    """(T, H, row stride) of a [T, H] tensor whose rows are contiguous."""
+    if x.dim() != 2:
+        raise ValueError(f"expected [rows, width], got {tuple(x.shape)}")
+    T, H = x.shape
+    if H > 1 and x.stride(1) != 1:
+        raise ValueError("rows have to be contiguous")
+    return T, H, (x.stride(0) if T > 1 else H)
+
+
+def orthrus_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Optional[torch.Tensor] = None,
+                    residual: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None,
+                    out_fp8: Optional[torch.Tensor] = None, out_scale: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """x [T,H] (rows may be strided; bf16, fp16 or fp32), weight [H] -> out [T,H]
+    and / or out_fp8 [T,H] e4m3 with out_scale [T,ceil(H/128)] fp32; with a
+    residual [T,H], x + residual is normed and written to sum_out."""
+    T, H, stride = _rows(x)
+    _same((weight, out, residual, sum_out), x.dtype)
+    _shape(weight, H)
+    for t in (out, residual, sum_out, out_fp8):
+        if t is not None:
+            _shape(t, T, H)
+    if out_fp8 is not None:
+        _same((out_fp8,), torch.float8_e4m3fn)
+    if out_scale is not None:
+        _same((out_scale,), torch.float32)
+        _shape(out_scale, T, (H + 127) // 128)
+    _dense(weight, out, residual, sum_out, out_fp8, out_scale)
+    dev, st = _where((x, weight, out, residual, sum_out, out_fp8, out_scale), stream)
+    _launch("orthrus_rmsnorm", dev, _code(x.dtype), x.data_ptr(), stride, _addr(residual), weight.data_ptr(), T, H,
+            eps, _addr(sum_out), _addr(out), _addr(out_fp8), _addr(out_scale), st)
+
+
+def orthrus_quantize_fp8(x: torch.Tensor, out_fp8: torch.Tensor, out_scale: torch.Tensor, stream=None) -> None:
+    """x [T,H] (rows may be strided) -> out_fp8 [T,H] e4m3 and out_scale
+    [T,ceil(H/128)] fp32, one scale per row and 128 columns."""
+    T, H, stride = _rows(x)
+    _shape(out_fp8, T, H)
+    _shape(out_scale, T, (H + 127) // 128)
+    _same((out_fp8,), torch.float8_e4m3fn)
+    _same((out_scale,), torch.float32)
+    _dense(out_fp8, out_scale)
+    dev, st = _where((x, out_fp8, out_scale), stream)
+    _launch("orthrus_quantize_fp8", dev, _code(x.dtype), x.data_ptr(), stride, T, H, out_fp8.data_ptr(),
+            out_scale.data_ptr(), st)
+
+
+def orthrus_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                       out: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """a [M,K] and w [N,K] e4m3 with scales a_scale [M,ceil(K/128)] and w_scale
+    [ceil(N/128),ceil(K/128)] fp32 -> out [M,N] (bf16, fp16 or fp32) = a w^T."""
+    M, K = a.shape
+    N = w.shape[0]
+    nk = (K + 127) // 128
+    _same((a, w), torch.float8_e4m3fn)
+    _same((a_scale, w_scale), torch.float32)
+    _shape(w, N, K)
+    _shape(a_scale, M, nk)
+    _shape(w_scale, (N + 127) // 128, nk)
+    _shape(out, M, N)
+    _dense(a, a_scale, w, w_scale, out, status)
+    dev, st = _where((a, a_scale, w, w_scale, out, status), stream)
+    _launch("orthrus_fp8_matmul", dev, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
+            _code(out.dtype), out.data_ptr(), _addr(status), st)
+
+
+def orthrus_rope_table(rot_dim: int, theta: float, kind: int = ROPE_PLAIN, factor: float = 1.0,
+                       orig_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(turns, magnitude): turns per position of the rot_dim / 2 pairs as a CPU
+    float64 tensor (upload it once), and the factor on the rotated values."""
+    turns = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    mag = ctypes.c_float()
+    rc = lib().orthrus_rope_table(kind, rot_dim, theta, factor, orig_len, beta_fast, beta_slow, turns.data_ptr(),
+                                  ctypes.addressof(mag))
+    _check("orthrus_rope_table", rc)
+    return turns, mag.value
+
+
+_Strides = ctypes.c_int64 * 8
+
+
+def _token_strides(t: torch.Tensor, lead):
+    """(token stride, head stride) of [*lead, H, D]: tokens evenly spaced, heads' elements contiguous."""
+    H, D = t.shape[-2:]
+    s = t.stride()
+    if D > 1 and s[-1] != 1:
+        raise ValueError("a head's elements have to be contiguous")
+    if len(lead) == 1:
+        return s[0], s[1]
+    if lead[0] > 1 and lead[1] > 1 and s[0] != lead[1] * s[1]:
+        raise ValueError("tokens have to be evenly spaced over sequences and block slots")
+    return (s[1] if lead[1] > 1 else s[0]), s[2]
+
+
+def _rope_common(q, k, q_out, turns, q_norm, k_norm, D, dtype):
+    rot = 2 * turns.shape[0]
+    _same((q, k, q_out, q_norm, k_norm), dtype)
+    _same((turns,), torch.float64)
+    for t in (q_norm, k_norm):
+        if t is not None:
+            _shape(t, D)
+    _dense(turns, q_norm, k_norm)
+    return rot
+
+
+def orthrus_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, turns: torch.Tensor,
+                 q_out: torch.Tensor, k_out: Optional[torch.Tensor] = None, layout: int = ROPE_HALF,
+                 magnitude: float = 1.0, q_norm: Optional[torch.Tensor] = None,
+                 k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    """q [T,Hq,D], k [T,Hkv,D] or None (tokens and heads may be strided) at
+    positions [T] int32 -> q_out, k_out (may be q and k themselves).  turns
+    [rot/2] float64 on the device and magnitude: from orthrus_rope_table."""
+    T, Hq, D = q.shape
+    rot = _rope_common(q, k, q_out, turns, q_norm, k_norm, D, q.dtype)
+    _same((positions,), torch.int32)
+    _shape(positions, T)
+    _shape(q_out, T, Hq, D)
+    lead, Hkv = (T,), 0
+    st4 = _token_strides(q, lead) + _token_strides(q_out, lead)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None:
+        Hkv = k.shape[1]
+        _shape(k, T, Hkv, D)
+        _shape(k_out, T, Hkv, D)
+        _same((k_out,), q.dtype)
+        st4 += _token_strides(k, lead) + _token_strides(k_out, lead)
+    else:
+        st4 += (0, 0, 0, 0)
+    _dense(positions)
+    dev, st = _where((q, k, positions, turns, q_out, k_out, q_norm, k_norm), stream)
+    _launch("orthrus_rope", dev, _code(q.dtype), layout, q.data_ptr(), q_out.data_ptr(), _addr(k), _addr(k_out),
+            _Strides(*st4), positions.data_ptr(), turns.data_ptr(), magnitude, T, Hq, Hkv, D, rot, _addr(q_norm),
+            _addr(k_norm), eps, st)
+
+
+def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                        turns: torch.Tensor, q_out: Optional[torch.Tensor], k_pages: torch.Tensor,
+                        v_pages: Optional[torch.Tensor], block_table: torch.Tensor, ctx_lens: torch.Tensor,
+                        layout: int = ROPE_HALF, magnitude: float = 1.0, q_norm: Optional[torch.Tensor] = None,
+                        k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        K: Optional[int] = None, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q [B,K,Hq,D], k and v [B,K,Hkv,D] (tokens and heads may be strided) at
+    positions ctx_lens[b] + i -> q_out, and rows of k_pages / v_pages
+    [num_pages,Hkv,page_size,D] through block_table [B,max_pages].  With k and v
+    None the keys already in those rows are rotated in place (give K where q is
+    None too)."""
+    P, Hkv, page, D = k_pages.shape
+    B, max_pages = block_table.shape
+    dtype = k_pages.dtype
+    rot = _rope_common(q, k, q_out, turns, q_norm, k_norm, D, dtype)
+    _same((v, v_pages), dtype)
+    _same((block_table, ctx_lens), torch.int32)
+    _shape(ctx_lens, B)
+    if (q is None) != (q_out is None) or (k is None) != (v is None):
+        raise ValueError("q and q_out, and k and v, go together")
+    n = q if q is not None else k
+    if n is not None:
+        K = n.shape[1]
+    if K is None:
+        raise ValueError("the number of tokens per sequence is not known: give K")
+    lead, Hq, st8 = (B, K), 0, ()
+    if q is not None:
+        Hq = q.shape[2]
+        _shape(q, B, K, Hq, D)
+        _shape(q_out, B, K, Hq, D)
+        st8 += _token_strides(q, lead) + _token_strides(q_out, lead)
+    else:
+        st8 += (0, 0, 0, 0)
+    if k is not None:
+        if v_pages is None:
+            raise ValueError("v needs v_pages")
+        _shape(k, B, K, Hkv, D)
+        _shape(v, B, K, Hkv, D)
+        st8 += _token_strides(k, lead) + _token_strides(v, lead)
+    else:
+        st8 += (0, 0, 0, 0)
+    if v_pages is not None:
+        _shape(v_pages, P, Hkv, page, D)
+    _dense(k_pages, v_pages, block_table, ctx_lens, status)
+    dev, st = _where((q, k, v, turns, q_out, k_pages, v_pages, block_table, ctx_lens, q_norm, k_norm, status), stream)
+    _launch("orthrus_rope_append", dev, _code(dtype), layout, _addr(q), _addr(q_out), _addr(k), _addr(v),
+            _Strides(*st8), turns.data_ptr(), magnitude, B, K, Hq, Hkv, D, rot, _addr(q_norm), _addr(k_norm), eps,
+            k_pages.data_ptr(), _addr(v_pages), P, page, block_table.data_ptr(), max_pages, ctx_lens.data_ptr(),
+            _addr(status), st)
+
+
+def orthrus_paged_attn_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().orthrus_paged_attn_workspace_size(B, Hq, Hkv, D))
+
+
+def orthrus_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                       ctx_lens: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, n_new: int = 0,
+                       scale: float = 0.0, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """q [B,Hq,D], pages [num_pages,Hkv,page_size,D] (bf16 or fp16), block_table
+    [B,max_pages] int32, ctx_lens [B] int32 -> out [B,Hq,D]: attention of one
+    token per sequence over keys [0, ctx_lens[b] + n_new)."""
+    B, Hq, D = q.shape
+    P, Hkv, page, _ = k_pages.shape
+    _same((k_pages, v_pages, out), q.dtype)
+    _same((block_table, ctx_lens), torch.int32)
+    _shape(k_pages, P, Hkv, page, D)
+    _shape(v_pages, P, Hkv, page, D)
+    _shape(out, B, Hq, D)
+    _shape(ctx_lens, B)
+    max_pages = block_table.shape[1]
+    _shape(block_table, B, max_pages)
+    _dense(q, k_pages, v_pages, block_table, ctx_lens, out, workspace, status)
+    dev, st = _where((q, k_pages, v_pages, block_table, ctx_lens, out, workspace, status), stream)
+    _launch("orthrus_paged_attn", dev, _code(q.dtype), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            block_table.data_ptr(), ctx_lens.data_ptr(), n_new, B, Hq, Hkv, D, P, page, max_pages, scale,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(status), st)

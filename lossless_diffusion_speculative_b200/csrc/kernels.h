@@ -92,6 +92,10 @@ inline size_t attn_ws_bytes(int slots, int rows, int D)
 bool encode_bf16_sw128(CUtensorMap *m, int rank, const void *base, const uint64_t *dims,
                        const uint64_t *strides, const uint32_t *box);
 
+// The same for 8-bit elements.
+bool encode_u8_sw128(CUtensorMap *m, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                     const uint32_t *box);
+
 cudaError_t launch_attn_simt(const AttnArgs &p, int grid, cudaStream_t st);
 cudaError_t launch_attn_combine(const AttnArgs &p, int grid_main, cudaStream_t st);
 

@@ -1,0 +1,583 @@
+// Attention of one new token per sequence over a paged KV cache, split over the
+// cache's length and joined in the same launch.
+//
+//     out[b,h] = sum_j softmax_j(scale <q[b,h], K[b,g,j]>) V[b,g,j],  j < len_b
+//
+// What bounds it: each key and value is used by the G = Hq / Hkv query heads of
+// its KV head only, 2 G flop per byte, so the keys and values are streamed once
+// from HBM and everything else has to hide behind that stream.  G <= 16 rows
+// would fill an eighth of a tcgen05 tile's 128 and pay its TMEM round trips per
+// tile, so the products run on mma.sync m16n8k16 with the heads as the 16 rows:
+// 48 such instructions per 16 keys x 128 dims (8 KB) against the ~350 cycles
+// the SM's share of HBM needs to deliver them.
+//
+// Work split: every sequence's keys are cut into tiles of 64; the tiles of all
+// (sequence, KV head, group of 16 heads) segments are laid end to end and cut
+// into equal contiguous ranges, one per block, computed on the device from
+// ctx_lens.  Each of the block's four warps takes 16 keys of a tile and runs its
+// own cp.async ring and its own running maximum and sum (no block-wide barrier
+// inside a segment); the four are combined through shared memory when the block
+// leaves a segment.  A segment that spans blocks is joined by the last of them
+// to arrive (a counter per segment), which adds the partials in block order.
+//
+// Numerics: q.k in fp32 from exact products, running maximum with a lazy
+// rescale (only when a row's maximum grows by more than 2^8), p = 2^(s - m) split
+// into two 16-bit terms p_hi + p_lo for the second product: one 16-bit p would
+// lose 2^-9 (bf16) per weight, the second term is free behind the stream.
+#include <math.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "kernels.h"
+#include "layer_ops.cuh"
+
+namespace orthrus {
+
+namespace paged {
+
+using namespace sm100;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStrip = 16;                       // keys per warp and tile
+constexpr int kTile = kWarps * kStrip;
+constexpr int kRows = 16;                        // query heads per segment (the MMA's M)
+constexpr int kMaxB = 4096;
+constexpr float kLazy = 8.f;                     // log2 units
+
+struct Args {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *block_table, *ctx_lens;
+    void *out;
+    int32_t *counters;                           // [B * segments], zero between calls
+    float *part_ml;                              // [2 * grid][kRows][2]: maximum, sum
+    float *part_o;                               // [2 * grid][rows][D], not normalised
+    int32_t *status;
+    int n_new, B, Hq, Hkv, G, HG;                // HG: groups of 16 heads per KV head
+    int num_pages, page_size, max_pages;
+    float scale_log2;
+};
+
+__device__ __forceinline__ int visible(const Args &p, int b, bool report)
+{
+    const int c = p.ctx_lens[b];
+    const int64_t n = (int64_t)c + p.n_new;
+    if (c < 0 || n > (int64_t)p.max_pages * p.page_size) {
+        if (report) raise_status(p.status, ORTHRUS_STATUS_CAPACITY);
+        return 0;
+    }
+    return (int)n;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool full)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Position in the flat tile order: sequence b, segment g (KV head x head
+// group), tile t of its n tiles.
+struct Pos {
+    int b, g, t, n, len;
+};
+
+// Shared memory of one block: the warps' rings, the running maxima and sums at
+// a segment's end, the rings' key masks, and after them the first flat tile of
+// every sequence (prefix, in tiles of one segment).
+template <int D> struct Layout {
+    static constexpr int kStripBytes = kStrip * D * 2;               // keys (or values) of a strip
+    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kRing = kWarps * kStages * 2 * kStripBytes;
+    static constexpr int kML = kWarps * kRows * 2 * 4;               // m, l per warp and row
+    static constexpr int kMask = kWarps * kStages * 4;
+    static constexpr int kFixed = kRing + kML + kMask;
+    // a warp's O of 16 rows takes the place of the strip it has just read
+    static_assert(2 * kStripBytes == kRows * D * 4, "O fits a stage");
+};
+
+// (blocks of D = 64 and 128 fit twice into an SM)
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(const Args p)
+{
+    using L = Layout<D>;
+    constexpr int kStages = L::kStages, CH = D / 8;                  // 16-byte chunks of a row
+    extern __shared__ __align__(128) uint8_t smem[];
+    float2 *comb_ml = reinterpret_cast<float2 *>(smem + L::kRing);   // [warp][row]
+    volatile uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::kRing + L::kML);
+    int *pre = reinterpret_cast<int *>(smem + L::kFixed);            // [B + 1]
+    __shared__ int flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int segs = p.Hkv * p.HG;
+    pdl_trigger();
+    pdl_wait();
+
+    // ---- the flat tile order: exclusive prefix of the sequences' tile counts
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int n = b < p.B ? (visible(p, b, blockIdx.x == 0) + kTile - 1) / kTile : 0;
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += y;
+            }
+            if (b < p.B) pre[b] = run + x - n;
+            run += __shfl_sync(~0u, x, 31);
+        }
+        if (lane == 0) pre[p.B] = run;
+    }
+    __syncthreads();
+    const int64_t total = (int64_t)pre[p.B] * segs;
+    // sequences with nothing to see: zeros
+    T *out = static_cast<T *>(p.out);
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (pre[b + 1] == pre[b])
+            for (int i = threadIdx.x; i < p.Hq * D; i += kThreads) out[(size_t)b * p.Hq * D + i] = from_f32<T>(0.f);
+    const int64_t P = total < gridDim.x ? total : gridDim.x;         // blocks with work
+    if (blockIdx.x >= P) return;
+    auto range = [&](int64_t c) { return c * total / P; };
+    const int64_t lo = range(blockIdx.x), hi = range(blockIdx.x + 1);
+
+    Pos cur;
+    {
+        int l = 0, r = p.B - 1;                                      // the sequence that holds flat tile lo
+        while (l < r) {
+            const int m = (l + r + 1) >> 1;
+            if ((int64_t)pre[m] * segs <= lo) l = m; else r = m - 1;
+        }
+        cur.b = l;
+        cur.n = pre[l + 1] - pre[l];
+        const int64_t o = lo - (int64_t)pre[l] * segs;
+        cur.g = (int)(o / cur.n);
+        cur.t = (int)(o - (int64_t)cur.g * cur.n);
+        cur.len = visible(p, l, false);
+    }
+    auto advance = [&](Pos &x) {
+        if (++x.t < x.n) return;
+        x.t = 0;
+        if (++x.g < segs) return;
+        x.g = 0;
+        do {
+            if (++x.b >= p.B) {
+                x.n = 0;
+                return;
+            }
+            x.n = pre[x.b + 1] - pre[x.b];
+        } while (x.n == 0);
+        x.len = visible(p, x.b, false);
+    };
+
+    // ---- this warp's ring
+    const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * L::kStripBytes;
+    const T *kp = static_cast<const T *>(p.k_pages), *vp = static_cast<const T *>(p.v_pages);
+    Pos iss = cur;
+    int64_t issued = lo;
+    // row offset (in rows of D) of the strip's key `lane & 15`, -1 where there is none
+    int64_t next_row = -1;
+    auto look_up = [&]() {
+        next_row = -1;
+        if (issued < hi) {
+            const int j = iss.t * kTile + warp * kStrip + (lane & 15);
+            if (j < iss.len) {
+                const int e = j / p.page_size;
+                const int page = p.block_table[(int64_t)iss.b * p.max_pages + e];
+                if (page >= 0 && page < p.num_pages)
+                    next_row = ((int64_t)page * p.Hkv + iss.g / p.HG) * p.page_size + (j - e * p.page_size);
+                else
+                    raise_status(p.status, ORTHRUS_STATUS_PAGE);
+            }
+        }
+    };
+    look_up();
+    auto issue = [&](int stage) {
+        const uint32_t dk = ring + stage * 2 * L::kStripBytes, dv = dk + L::kStripBytes;
+        const uint32_t m = __ballot_sync(~0u, next_row >= 0) & 0xffffu;
+        if (lane == 0) masks[warp * kStages + stage] = m;
+        if (m) {
+#pragma unroll
+            for (int i = 0; i < kStrip * CH / 32; ++i) {
+                const int id = i * 32 + lane, r = id / CH, c = id % CH;
+                const int64_t row = __shfl_sync(~0u, next_row, r);
+                const uint32_t o = (uint32_t)(r * D * 2 + ((c ^ (r & 7)) << 4));
+                const int64_t src = (row < 0 ? 0 : row) * D + c * 8;
+                cp_async16(dk + o, kp + src, row >= 0);
+                cp_async16(dv + o, vp + src, row >= 0);
+            }
+        }
+        if (issued < hi) {
+            advance(iss);
+            ++issued;
+        }
+        look_up();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        issue(s);
+        cp_commit();
+    }
+
+    // ---- per-segment state
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    auto begin = [&]() {
+        const int g = cur.g / p.HG, h0 = (cur.g - g * p.HG) * kRows;
+        const int r0 = h0 + (lane >> 2), r1 = r0 + 8;
+        const T *q = static_cast<const T *>(p.q) + ((size_t)cur.b * p.Hq + g * p.G) * D + (lane & 3) * 2;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            qf[k][0] = r0 < p.G ? *reinterpret_cast<const uint32_t *>(q + r0 * D + k * 16) : 0u;
+            qf[k][1] = r1 < p.G ? *reinterpret_cast<const uint32_t *>(q + r1 * D + k * 16) : 0u;
+            qf[k][2] = r0 < p.G ? *reinterpret_cast<const uint32_t *>(q + r0 * D + k * 16 + 8) : 0u;
+            qf[k][3] = r1 < p.G ? *reinterpret_cast<const uint32_t *>(q + r1 * D + k * 16 + 8) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+    };
+    begin();
+
+    int stage = 0;
+    for (int64_t x = lo; x < hi; ++x) {
+        cp_wait<kStages - 2>();
+        __syncwarp();              // (also: every lane is done with the stage that this iteration issues into)
+        const uint32_t mask = masks[warp * kStages + stage];
+        const uint32_t sk = ring + stage * 2 * L::kStripBytes, sv = sk + L::kStripBytes;
+        if (mask) {
+            float s[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            {
+                // matrices: keys 0-7 | dims lo, hi, then keys 8-15 | dims lo, hi
+                const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t b[4];
+                    ldsm4(b, sk + r * D * 2 + (((2 * k + cc) ^ (r & 7)) << 4));
+                    mma<T>(s[0], qf[k], b[0], b[1]);
+                    mma<T>(s[1], qf[k], b[2], b[3]);
+                }
+            }
+            // columns of this thread: keys 2 (lane & 3) + {0, 1} of each half
+            const uint32_t mk = mask >> ((lane & 3) * 2);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[i][j] = (mk >> (8 * i + (j & 1))) & 1u ? s[i][j] * p.scale_log2 : -INFINITY;
+            float a0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+            float a1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                a0 = fmaxf(a0, __shfl_xor_sync(~0u, a0, d));
+                a1 = fmaxf(a1, __shfl_xor_sync(~0u, a1, d));
+            }
+            if (__any_sync(~0u, a0 > m0 + kLazy || a1 > m1 + kLazy)) {
+                const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+                const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f0;
+                    o[i][2] *= f1;
+                    o[i][3] *= f1;
+                }
+                l0 *= f0;
+                l1 *= f1;
+                m0 = n0;
+                m1 = n1;
+            }
+            // a row whose scores so far are all -inf keeps the weights at zero
+            const float e0 = m0 == -INFINITY ? 0.f : m0, e1 = m1 == -INFINITY ? 0.f : m1;
+            uint32_t hi_[4], lo_[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float e = h ? e1 : e0;
+                    const float x0 = fast_exp2(s[i][2 * h] - e), x1 = fast_exp2(s[i][2 * h + 1] - e);
+                    if (h) l1 += x0 + x1; else l0 += x0 + x1;
+                    const uint32_t w = pack2<T>(x0, x1);
+                    const float2 back = unpack2<T>(w);
+                    hi_[2 * i + h] = w;
+                    lo_[2 * i + h] = pack2<T>(x0 - back.x, x1 - back.y);
+                }
+            }
+            // matrices: dims lo | keys 0-7, 8-15, then dims hi | keys 0-7, 8-15
+            const int r = lane & 15, cc = lane >> 4;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t b[4];
+                ldsm4_t(b, sv + r * D * 2 + (((2 * d + cc) ^ (r & 7)) << 4));
+                mma<T>(o[2 * d], hi_, b[0], b[1]);
+                mma<T>(o[2 * d + 1], hi_, b[2], b[3]);
+                mma<T>(o[2 * d], lo_, b[0], b[1]);
+                mma<T>(o[2 * d + 1], lo_, b[2], b[3]);
+            }
+        }
+        issue((stage + kStages - 1) % kStages);
+        cp_commit();
+
+        if (cur.t + 1 == cur.n || x + 1 == hi) {   // the block leaves this segment
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                l0 += __shfl_xor_sync(~0u, l0, d);
+                l1 += __shfl_xor_sync(~0u, l1, d);
+            }
+            const int rowsG = p.G - (cur.g % p.HG) * kRows, rows = rowsG < kRows ? rowsG : kRows;
+            const int r0 = lane >> 2, r1 = r0 + 8;
+            // the stage just read holds O now (its next load is issued an iteration
+            // later); 8-value chunk i of row r sits at i ^ (r & 7)
+            auto comb_o = [&](int w) {
+                return reinterpret_cast<float *>(smem + ((w * kStages + stage) * 2) * L::kStripBytes);
+            };
+            float *c0 = comb_o(warp) + r0 * D, *c1 = comb_o(warp) + r1 * D;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const int at = (i ^ r0) * 8 + (lane & 3) * 2;
+                if (r0 < rows) *reinterpret_cast<float2 *>(c0 + at) = make_float2(o[i][0], o[i][1]);
+                if (r1 < rows) *reinterpret_cast<float2 *>(c1 + at) = make_float2(o[i][2], o[i][3]);
+            }
+            if ((lane & 3) == 0) {
+                comb_ml[warp * kRows + r0] = make_float2(m0, l0);
+                comb_ml[warp * kRows + r1] = make_float2(m1, l1);
+            }
+            __syncthreads();
+            const int64_t s0 = (int64_t)pre[cur.b] * segs + (int64_t)cur.g * cur.n;      // the segment's flat tiles
+            const bool whole = lo <= s0 && hi >= s0 + cur.n;
+            const int g = cur.g / p.HG, h0 = (cur.g - g * p.HG) * kRows;
+            T *dst = out + ((size_t)cur.b * p.Hq + g * p.G + h0) * D;
+            const size_t slot = 2 * (size_t)blockIdx.x + (lo < s0 ? 1 : 0);
+            for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, comb_ml[w * kRows + r].x);
+                const float E = M == -INFINITY ? 0.f : M;
+                float l = 0.f;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 ml = comb_ml[w * kRows + r];
+                    const float f = fast_exp2(ml.x - E);
+                    const float4 v = *reinterpret_cast<const float4 *>(comb_o(w) + r * D + ((d >> 3) ^ (r & 7)) * 8 + (d & 7));
+                    l += ml.y * f;
+                    a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+                }
+                if (whole) {
+                    const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;           // (NaN stays NaN)
+                    *reinterpret_cast<uint2 *>(dst + r * D + d) =
+                        make_uint2(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv));
+                } else {
+                    *reinterpret_cast<float4 *>(p.part_o + (slot * kRows + r) * D + d) = a;
+                    if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * kRows + r) * 2) = make_float2(M, l);
+                }
+            }
+            if (!whole) {
+                // blocks [c0, c1] hold the segment; the last to arrive joins it
+                const int c_first = (int)(((s0 + 1) * P - 1) / total), c_last = (int)(((s0 + cur.n) * P - 1) / total);
+                const int seg = cur.b * segs + cur.g, n = c_last - c_first + 1;
+                __syncthreads();                   // every partial store of the block, before the release
+                if (threadIdx.x == 0) {
+                    const int old = counter_fetch_add_acq_rel(p.counters + seg, 1);
+                    flag = old == n - 1;
+                    if (flag) p.counters[seg] = 0;
+                }
+                __syncthreads();
+                if (flag) {
+                    auto slot_of = [&](int j) {
+                        const int64_t c = c_first + j;
+                        return 2 * (size_t)c + (range(c) < s0 ? 1 : 0);
+                    };
+                    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+                        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+                        float M = -INFINITY, l = 0.f;
+                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int j = 0; j < n; ++j)
+                            M = fmaxf(M, __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) * kRows + r) * 2)).x);
+                        const float E = M == -INFINITY ? 0.f : M;
+                        for (int j = 0; j < n; ++j) {
+                            const size_t sl = slot_of(j) * kRows + r;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + sl * 2));
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + sl * D + d));
+                            const float f = fast_exp2(ml.x - E);
+                            l += ml.y * f;
+                            a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+                        }
+                        const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;
+                        *reinterpret_cast<uint2 *>(dst + r * D + d) =
+                            make_uint2(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv));
+                    }
+                }
+            }
+            __syncthreads();                       // the combine buffer and the flag are free again
+            if (x + 1 < hi) {
+                advance(cur);
+                begin();
+            }
+        } else {
+            ++cur.t;
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+}
+
+// Largest page-table geometry and the block count the launch uses.
+inline int grid_of(int D, int sms) { return D == 256 ? sms : 2 * sms; }
+
+struct Plan {
+    int grid;
+    size_t counters, ml, o, total;
+};
+
+inline Plan plan(int B, int Hq, int Hkv, int D, int sms)
+{
+    Plan w;
+    const int G = Hq / Hkv, HG = (G + kRows - 1) / kRows;
+    w.grid = grid_of(D, sms);
+    w.counters = ((size_t)B * Hkv * HG * sizeof(int32_t) + 255) & ~(size_t)255;
+    w.ml = w.counters;
+    w.o = w.ml + (((size_t)2 * w.grid * kRows * 2 * sizeof(float) + 255) & ~(size_t)255);
+    w.total = w.o + (size_t)2 * w.grid * kRows * D * sizeof(float);
+    return w;
+}
+
+constexpr int kMaxDevices = 64;
+
+template <typename T, int D> bool smem_ready()
+{
+    static std::once_flag once[kMaxDevices];
+    static bool ok[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    std::call_once(once[dev], [dev] {
+        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Layout<D>::kFixed + (kMaxB + 1) * (int)sizeof(int)) == cudaSuccess;
+        if (!ok[dev]) cudaGetLastError();
+    });
+    return ok[dev];
+}
+
+template <typename T, int D> cudaError_t launch(const Args &a, int grid, cudaStream_t st)
+{
+    if (!smem_ready<T, D>()) return cudaErrorInvalidValue;
+    const size_t smem = Layout<D>::kFixed + ((size_t)a.B + 1) * sizeof(int);
+    return launch_pdl(paged_attn_kernel<T, D>, dim3(grid), kThreads, smem, st, a);
+}
+
+template <typename T> cudaError_t launch_d(const Args &a, int D, int grid, cudaStream_t st)
+{
+    return D == 64 ? launch<T, 64>(a, grid, st) : D == 128 ? launch<T, 128>(a, grid, st) : launch<T, 256>(a, grid, st);
+}
+
+int current_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
+bool shape_ok(int B, int Hq, int Hkv, int D) { return B > 0 && Hq > 0 && Hkv > 0 && D > 0 && Hq % Hkv == 0; }
+bool shape_supported(int B, int Hq, int D)
+{
+    return B <= kMaxB && (D == 64 || D == 128 || D == 256) && Hq <= 65536;
+}
+
+}  // namespace paged
+
+}  // namespace orthrus
+
+using namespace orthrus;
+
+extern "C" size_t orthrus_paged_attn_workspace_size(int B, int Hq, int Hkv, int D)
+{
+    if (!paged::shape_ok(B, Hq, Hkv, D) || !paged::shape_supported(B, Hq, D)) return 0;
+    const int sms = paged::current_sms();
+    return sms > 0 ? paged::plan(B, Hq, Hkv, D, sms).total : 0;
+}
+
+extern "C" int orthrus_paged_attn(orthrus_dtype dtype, const void *q, const void *k_pages, const void *v_pages,
+                                  const int32_t *block_table, const int32_t *ctx_lens, int n_new, int B, int Hq, int Hkv,
+                                  int D, int num_pages, int page_size, int max_pages, float scale, void *out,
+                                  void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
+{
+    if (!q || !k_pages || !v_pages || !block_table || !ctx_lens || !out) return ORTHRUS_ERR_ARG;
+    if (!paged::shape_ok(B, Hq, Hkv, D) || n_new < 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0)
+        return ORTHRUS_ERR_ARG;
+    if (!(scale == scale) || isinf(scale)) return ORTHRUS_ERR_ARG;
+    if (dtype != ORTHRUS_BF16 && dtype != ORTHRUS_F16) return dtype == ORTHRUS_F32 ? ORTHRUS_ERR_UNSUPPORTED : ORTHRUS_ERR_ARG;
+    if (!paged::shape_supported(B, Hq, D)) return ORTHRUS_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page_size > (1ll << 31) - 128 ||
+        ((int64_t)max_pages * page_size / paged::kTile + 1) * B >= (1ll << 31))
+        return ORTHRUS_ERR_UNSUPPORTED;          // (positions and the tile prefix are 32-bit)
+    if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out | (uintptr_t)workspace) & 15u)
+        return ORTHRUS_ERR_ALIGN;
+    const int sms = paged::current_sms();
+    if (sms <= 0) return ORTHRUS_ERR_DEVICE;
+    const paged::Plan w = paged::plan(B, Hq, Hkv, D, sms);
+    if (!workspace || workspace_bytes < w.total) return ORTHRUS_ERR_WORKSPACE;
+    paged::Args a;
+    a.q = q;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.block_table = block_table;
+    a.ctx_lens = ctx_lens;
+    a.out = out;
+    char *ws = static_cast<char *>(workspace);
+    a.counters = reinterpret_cast<int32_t *>(ws);
+    a.part_ml = reinterpret_cast<float *>(ws + w.ml);
+    a.part_o = reinterpret_cast<float *>(ws + w.o);
+    a.status = status;
+    a.n_new = n_new;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.HG = (a.G + paged::kRows - 1) / paged::kRows;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * kLog2e;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == ORTHRUS_BF16 ? paged::launch_d<__nv_bfloat16>(a, D, w.grid, st)
+                                                : paged::launch_d<__half>(a, D, w.grid, st);
+    return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
+}

@@ -31,8 +31,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 
 }  // namespace
 
-bool encode_bf16_sw128(CUtensorMap *m, int rank, const void *base, const uint64_t *dims,
-                       const uint64_t *strides, const uint32_t *box)
+static bool encode_sw128(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,
+                         const uint64_t *strides, const uint32_t *box)
 {
     auto fn = encode_fn();
     if (!fn || rank < 1 || rank > 5) return false;
@@ -44,9 +44,21 @@ bool encode_bf16_sw128(CUtensorMap *m, int rank, const void *base, const uint64_
         e[i] = 1;
         if (i + 1 < rank) st[i] = strides[i];
     }
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, st, b,
+    return fn(m, type, (cuuint32_t)rank, const_cast<void *>(base), d, st, b,
               e, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_bf16_sw128(CUtensorMap *m, int rank, const void *base, const uint64_t *dims,
+                       const uint64_t *strides, const uint32_t *box)
+{
+    return encode_sw128(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base, dims, strides, box);
+}
+
+bool encode_u8_sw128(CUtensorMap *m, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                     const uint32_t *box)
+{
+    return encode_sw128(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, base, dims, strides, box);
 }
 
 }  // namespace orthrus
