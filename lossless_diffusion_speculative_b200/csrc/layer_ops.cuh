@@ -70,6 +70,42 @@ template <typename T> __device__ __forceinline__ void store8(T *p, const float (
     }
 }
 
+// Eight consecutive values as loaded (not yet converted), so that loads can be
+// in flight without holding fp32 registers.
+template <typename T> struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+template <typename T> __device__ __forceinline__ Raw8<T> load_raw(const T *p)
+{
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    return r;
+}
+template <typename T> __device__ __forceinline__ void unpack8(const Raw8<T> &r, float2 (&x)[4])
+{
+    if constexpr (sizeof(T) == 2) {
+        x[0] = unpack2<T>(r.w[0].x), x[1] = unpack2<T>(r.w[0].y);
+        x[2] = unpack2<T>(r.w[0].z), x[3] = unpack2<T>(r.w[0].w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[2 * i] = make_float2(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+            x[2 * i + 1] = make_float2(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+        }
+    }
+}
+template <typename T> __device__ __forceinline__ void store8(T *p, const float2 (&x)[4])
+{
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y), pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y));
+    } else {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+    }
+}
+
 // Host: the size of an orthrus_dtype's element, 0 for anything else.
 inline int elem_size(int dtype)
 {

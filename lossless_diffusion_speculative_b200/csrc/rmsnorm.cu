@@ -44,10 +44,157 @@ __device__ __forceinline__ float lanes_max(float v, int o)
     return v;
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return fmaxf(amax / 448.0f, 1.17549435e-38f); }
+// Scale of a group from its maximum, and the scale's reciprocal.  The division
+// is multiplication by the rounded reciprocal and one exact-remainder step
+// (fma), which gives the correctly rounded quotient.
+struct Scale {
+    float s, inv;
+};
+__device__ __forceinline__ Scale scale_of(float amax)
+{
+    const float r = 1.0f / 448.0f, q = amax * r;
+    Scale o;
+    o.s = fmaxf(amax < INFINITY ? fmaf(fmaf(-q, 448.0f, amax), r, q) : amax, 1.17549435e-38f);
+    float a;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(o.s));
+    const float b = fmaf(fmaf(-o.s, a, 1.0f), a, a);
+    o.inv = o.s < INFINITY ? b : 0.f;
+    return o;
+}
 
-template <typename T, int V, int NC, bool NORM, int MAXT>
-__global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p)
+// y / scale, rounded once (the remainder step again), as e4m3: two values, low
+// byte first.  With an infinite scale the quotient is y * 0.
+__device__ __forceinline__ uint32_t quotient2(float2 y, const Scale &sc)
+{
+    const float2 i = make_float2(sc.inv, sc.inv), ns = make_float2(-sc.s, -sc.s);
+    float2 q = sm100::fmul2(y, i);
+    if (sc.inv != 0.f) q = sm100::ffma2(sm100::ffma2(ns, q, y), i, q);
+    return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+// ---- vector path
+//
+// A row belongs to W warps (W <= 32, a power of two with the norm), a lane
+// holds NC chunks of 8 consecutive values.  Blocks are resident for the whole
+// call and walk the rows, the next row's loads issued (unconverted) before the
+// current one is worked on, so that the memory never waits for the arithmetic;
+// the weights stay in registers.  Without the norm a warp's part of a row is a
+// unit of its own.
+template <typename T, int NC, bool NORM, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_rows_kernel(const NormArgs p)
+{
+    __shared__ float part[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int W = p.W, H = p.H, groups = (H + 127) >> 7;
+    sm100::pdl_trigger();
+    sm100::pdl_wait();
+
+    const T *x = static_cast<const T *>(p.x), *res = static_cast<const T *>(p.residual);
+    const bool add = NORM && p.residual != nullptr;
+    // unit = (row, part of the row); a block's warps take consecutive units
+    const unsigned units = (unsigned)p.T * W, step = gridDim.x * warps;
+    unsigned unit = blockIdx.x * warps + warp;
+    Raw8<T> nx[NC], nr[NORM ? NC : 1], wt[NORM ? NC : 1];
+    unsigned row = unit / W;
+    int c0 = (int)(unit - row * W) * 256 + lane * 8;                  // columns c0 + 256 W c of chunk c
+    auto fetch = [&](unsigned r, int col, bool live) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int k = col + c * W * 256;
+            nx[c] = Raw8<T>{};
+            if (live && k < H) nx[c] = load_raw(x + (int64_t)r * p.x_stride + k);
+            if constexpr (NORM) {
+                if (add) {
+                    nr[c] = Raw8<T>{};
+                    if (live && k < H) nr[c] = load_raw(res + (int64_t)r * H + k);
+                }
+            }
+        }
+    };
+    fetch(row, c0, unit < units);
+    if constexpr (NORM) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            wt[c] = Raw8<T>{};
+            if (c0 + c * W * 256 < H) wt[c] = load_raw(static_cast<const T *>(p.weight) + c0 + c * W * 256);
+        }
+    }
+    // (with the norm every warp of a block makes the same number of rounds)
+    const unsigned first = blockIdx.x * warps;
+    for (unsigned it = 0; (NORM ? first + it * step : unit) < units; ++it) {
+        const bool live = unit < units;
+        float2 s[NC][4];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) unpack8<T>(nx[c], s[c]);
+        if constexpr (NORM) {
+            if (add) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    float2 a[4];
+                    unpack8<T>(nr[c], a);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[c][j] = sm100::fadd2(s[c][j], a[j]);
+                }
+            }
+        }
+        const unsigned r = row;
+        const int k0 = c0;
+        unit += step;
+        row = unit / W;
+        c0 = (int)(unit - row * W) * 256 + lane * 8;                  // (with the norm: unchanged, W divides the step)
+        fetch(row, c0, unit < units);
+        if constexpr (NORM) {
+            float2 q2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                if (add && live && k0 + c * W * 256 < H)
+                    store8(static_cast<T *>(p.sum_out) + (int64_t)r * H + k0 + c * W * 256, s[c]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q2 = sm100::ffma2(s[c][j], s[c][j], q2);
+            }
+            float q = warp_sum(q2.x + q2.y);
+            if (W > 1) {
+                if (lane == 0) part[it & 1][warp] = q;
+                __syncthreads();
+                q = 0.f;
+                const int w0 = warp & ~(W - 1);
+                for (int w = 0; w < W; ++w) q += part[it & 1][w0 + w];
+            }
+            const float inv = 1.0f / sqrtf(q / (float)H + p.eps);
+            const float2 i2 = make_float2(inv, inv);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float2 w[4];
+                unpack8<T>(wt[c], w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[c][j] = sm100::fmul2(sm100::fmul2(s[c][j], i2), w[j]);
+                if (p.out && live && k0 + c * W * 256 < H)
+                    store8(static_cast<T *>(p.out) + (int64_t)r * H + k0 + c * W * 256, s[c]);
+            }
+        }
+        if (!NORM || p.out_fp8) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int k = k0 + c * W * 256;
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = sm100::fmax3(m, fabsf(s[c][j].x), fabsf(s[c][j].y));
+                const Scale sc = scale_of(lanes_max(m, 8));
+                const uint32_t lo = quotient2(s[c][0], sc) | (quotient2(s[c][1], sc) << 16);
+                const uint32_t hi = quotient2(s[c][2], sc) | (quotient2(s[c][3], sc) << 16);
+                if (live && k < H) {
+                    *reinterpret_cast<uint2 *>(p.out_fp8 + (int64_t)r * H + k) = make_uint2(lo, hi);
+                    if ((lane & 15) == 0) p.out_scale[(int64_t)r * groups + (k >> 7)] = sc.s;
+                }
+            }
+        }
+    }
+}
+
+// ---- element path: rows that are not 16-byte aligned, or whose width is not a
+// multiple of 8.  The same parts of a row, four strips of 32 lanes per group.
+template <typename T, int NC, bool NORM, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
 {
     __shared__ float part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -62,53 +209,31 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p)
     sm100::pdl_wait();
 
     // column of value j of chunk c: chunk c of warp wr covers 256 columns
-    auto col = [&](int c, int j) { return (c * W + wr) * 256 + (V == 8 ? lane * 8 + j : j * 32 + lane); };
+    auto col = [&](int c, int j) { return (c * W + wr) * 256 + j * 32 + lane; };
     const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
-    const T *r = static_cast<const T *>(p.residual) + row * H;
     float s[NC][8];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[c][j] = 0.f;
-        if (V == 8) {
-            if (live && col(c, 0) < H) load8(x + col(c, 0), s[c]);
-        } else {
+        for (int j = 0; j < 8; ++j) s[c][j] = live && col(c, j) < H ? to_f32<T>(x[col(c, j)]) : 0.f;
+    if constexpr (NORM) {
+        if (p.residual) {
+            const T *r = static_cast<const T *>(p.residual) + row * H;
+            T *so = static_cast<T *>(p.sum_out) + row * H;
+            float a[NC][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (live && col(c, j) < H) s[c][j] = to_f32<T>(x[col(c, j)]);
-        }
-    }
-    if (NORM && p.residual) {
-        T *so = static_cast<T *>(p.sum_out) + row * H;
-        float a[NC][8];
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (V == 8) {
-                if (live && col(c, 0) < H) load8(r + col(c, 0), a[c]);
-            } else {
+                for (int j = 0; j < 8; ++j) a[c][j] = live && col(c, j) < H ? to_f32<T>(r[col(c, j)]) : 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (live && col(c, j) < H) a[c][j] = to_f32<T>(r[col(c, j)]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (V == 8) {
-                if (!live || col(c, 0) >= H) continue;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s[c][j] += a[c][j];
-                store8(so + col(c, 0), s[c]);
-            } else {
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (live && col(c, j) < H) {
                         s[c][j] += a[c][j];
                         so[col(c, j)] = from_f32<T>(s[c][j]);
                     }
-            }
         }
-    }
-    if (NORM) {
         float q = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -124,29 +249,17 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p)
         const float inv = 1.0f / sqrtf(q / (float)H + p.eps);
         const T *wt = static_cast<const T *>(p.weight);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float w[8];
-            if (V == 8) {
-                if (col(c, 0) < H) load8(wt + col(c, 0), w);
-            }
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (V != 8) w[j] = col(c, j) < H ? to_f32<T>(wt[col(c, j)]) : 0.f;
-                s[c][j] = col(c, j) < H ? s[c][j] * inv * w[j] : 0.f;
-            }
-        }
-    }
-    if (NORM && p.out && live) {
-        T *o = static_cast<T *>(p.out) + row * H;
+            for (int j = 0; j < 8; ++j)
+                s[c][j] = col(c, j) < H ? s[c][j] * inv * to_f32<T>(wt[col(c, j)]) : 0.f;
+        if (p.out && live) {
+            T *o = static_cast<T *>(p.out) + row * H;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            if (V == 8) {
-                if (col(c, 0) < H) store8(o + col(c, 0), s[c]);
-            } else {
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     if (col(c, j) < H) o[col(c, j)] = from_f32<T>(s[c][j]);
-            }
         }
     }
     if (!NORM || p.out_fp8) {
@@ -155,56 +268,51 @@ __global__ void __launch_bounds__(MAXT) rmsnorm_kernel(const NormArgs p)
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int g0 = ((c * W + wr) * 256) >> 7;               // first of the chunk's two groups
-            if (V == 8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 float m = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(s[c][j]));
-                const float sc = scale_of(lanes_max(m, 8)), inv = 1.0f / sc;
-                if (!live || col(c, 0) >= H) continue;
-                uint32_t w[2];
+                for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(s[c][4 * h + j]));
+                const Scale sc = scale_of(lanes_max(m, 16));
+                if (!live) continue;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(s[c][4 * h] * inv, s[c][4 * h + 1] * inv),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-                        make_float2(s[c][4 * h + 2] * inv, s[c][4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-                    w[h] = lo | (hi << 16);
+                for (int j = 4 * h; j < 4 * h + 4; j += 2) {
+                    const uint32_t v = quotient2(make_float2(s[c][j], s[c][j + 1]), sc);
+                    if (col(c, j) < H) o[col(c, j)] = (uint8_t)v;
+                    if (col(c, j + 1) < H) o[col(c, j + 1)] = (uint8_t)(v >> 8);
                 }
-                *reinterpret_cast<uint2 *>(o + col(c, 0)) = make_uint2(w[0], w[1]);
-                if ((lane & 15) == 0) os[g0 + (lane >> 4)] = sc;
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float m = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(s[c][4 * h + j]));
-                    const float sc = scale_of(lanes_max(m, 16)), inv = 1.0f / sc;
-                    if (!live) continue;
-#pragma unroll
-                    for (int j = 4 * h; j < 4 * h + 4; ++j)
-                        if (col(c, j) < H) o[col(c, j)] = __nv_cvt_float_to_fp8(s[c][j] * inv, __NV_SATFINITE, __NV_E4M3);
-                    if (lane == 0 && (g0 + h) * 128 < H) os[g0 + h] = sc;
-                }
+                if (lane == 0 && (g0 + h) * 128 < H) os[g0 + h] = sc.s;
             }
         }
     }
 }
 
-template <typename T, int V, int NC, bool NORM> cudaError_t launch_norm(const NormArgs &a, cudaStream_t st)
+template <typename T, int NC, bool NORM> cudaError_t launch_norm(const NormArgs &a, bool vec, int sms, cudaStream_t st)
 {
     const int warps = NORM && a.W > 8 ? a.W : 8;
-    const dim3 grid((unsigned)(((int64_t)a.T * a.W + warps - 1) / warps));
-    if (warps > 8) return launch_pdl(rmsnorm_kernel<T, V, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
-    return launch_pdl(rmsnorm_kernel<T, V, NC, NORM, 256>, grid, warps * 32, 0, st, a);
+    int64_t blocks = ((int64_t)a.T * a.W + warps - 1) / warps;
+    if (!vec) {
+        const dim3 grid((unsigned)blocks);
+        if constexpr (NORM)
+            if (warps > 8) return launch_pdl(norm_any_kernel<T, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
+        return launch_pdl(norm_any_kernel<T, NC, NORM, 256>, grid, warps * 32, 0, st, a);
+    }
+    const int64_t resident = (int64_t)sms * (warps > 8 ? 1 : NORM ? 2 : 4);
+    const dim3 grid((unsigned)(blocks < resident ? blocks : resident));
+    if constexpr (NORM) {
+        if (warps > 16) return launch_pdl(norm_rows_kernel<T, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
+        if (warps > 8) return launch_pdl(norm_rows_kernel<T, NC, NORM, 512>, grid, warps * 32, 0, st, a);
+    }
+    return launch_pdl(norm_rows_kernel<T, NC, NORM, 256>, grid, warps * 32, 0, st, a);
 }
 
-template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, bool vec, cudaStream_t st)
+template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, bool vec, int sms, cudaStream_t st)
 {
     // Chunks per lane and warps per row: few rows spread a row over as many
     // warps as it has chunks (latency); many rows give a lane up to four chunks
     // (more loads in flight, fewer partial sums).
     const int chunks = (a.H + 255) / 256;
-    int nc = a.T <= 296 ? 1 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+    int nc = a.T <= 2 * sms ? 1 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
     while (NORM && nc < 4 && nc * 32 < chunks) nc *= 2;
     a.W = (chunks + nc - 1) / nc;
     if (NORM) {                                  // a block holds whole rows
@@ -212,13 +320,9 @@ template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, bool vec
         while (w < a.W) w *= 2;
         a.W = w;
     }
-    if (vec)
-        return nc == 1   ? launch_norm<T, 8, 1, NORM>(a, st)
-               : nc == 2 ? launch_norm<T, 8, 2, NORM>(a, st)
-                         : launch_norm<T, 8, 4, NORM>(a, st);
-    return nc == 1   ? launch_norm<T, 1, 1, NORM>(a, st)
-           : nc == 2 ? launch_norm<T, 1, 2, NORM>(a, st)
-                     : launch_norm<T, 1, 4, NORM>(a, st);
+    return nc == 1   ? launch_norm<T, 1, NORM>(a, vec, sms, st)
+           : nc == 2 ? launch_norm<T, 2, NORM>(a, vec, sms, st)
+                     : launch_norm<T, 4, NORM>(a, vec, sms, st);
 }
 
 template <bool NORM> int norm_call(int dtype, NormArgs &a, void *stream)
@@ -231,14 +335,14 @@ template <bool NORM> int norm_call(int dtype, NormArgs &a, void *stream)
         return ORTHRUS_ERR_ALIGN;
     if ((uintptr_t)a.out_scale & 3u) return ORTHRUS_ERR_ALIGN;
     const bool vec = (ptrs & 15u) == 0 && a.H % 8 == 0 && a.x_stride % 8 == 0;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ORTHRUS_ERR_DEVICE;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (sms <= 0) return ORTHRUS_ERR_DEVICE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t r;
-    if (dtype == ORTHRUS_BF16)
-        r = launch_norm_v<__nv_bfloat16, NORM>(a, vec, st);
-    else if (dtype == ORTHRUS_F16)
-        r = launch_norm_v<__half, NORM>(a, vec, st);
-    else
-        r = launch_norm_v<float, NORM>(a, vec, st);
+    const cudaError_t r = dtype == ORTHRUS_BF16  ? launch_norm_v<__nv_bfloat16, NORM>(a, vec, sms, st)
+                          : dtype == ORTHRUS_F16 ? launch_norm_v<__half, NORM>(a, vec, sms, st)
+                                                 : launch_norm_v<float, NORM>(a, vec, sms, st);
     return r == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
 }
 
@@ -257,6 +361,7 @@ extern "C" int orthrus_rmsnorm(orthrus_dtype dtype, const void *x, int64_t x_str
         return ORTHRUS_ERR_ARG;
     if ((!out && !out_fp8) || x_stride < (T > 1 ? H : 0)) return ORTHRUS_ERR_ARG;
     if (H > ORTHRUS_MAX_NORM_WIDTH) return ORTHRUS_ERR_UNSUPPORTED;
+    if ((int64_t)T * 32 >= (1ll << 31)) return ORTHRUS_ERR_UNSUPPORTED;                  // (units of work are 32-bit)
     // rows of x that are not dense must not be written through another stride
     if (x_stride != H && T > 1 && (sum_out == x || out == x)) return ORTHRUS_ERR_ARG;
     NormArgs a = {x, residual, weight, x_stride, sum_out, out, static_cast<uint8_t *>(out_fp8), out_scale, T, H, 1, eps};
@@ -269,6 +374,6 @@ extern "C" int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t 
     if (!x || !out_fp8 || !out_scale || !elem_size(dtype) || T <= 0 || H <= 0) return ORTHRUS_ERR_ARG;
     if (x_stride < (T > 1 ? H : 0)) return ORTHRUS_ERR_ARG;
     NormArgs a = {x, nullptr, nullptr, x_stride, nullptr, nullptr, static_cast<uint8_t *>(out_fp8), out_scale, T, H, 1, 0.f};
-    if ((int64_t)T * ((H + 255) / 256) >= (8ll << 31)) return ORTHRUS_ERR_UNSUPPORTED;   // (blocks of the grid)
+    if ((int64_t)T * ((H + 255) / 256) >= (1ll << 31)) return ORTHRUS_ERR_UNSUPPORTED;   // (units of work are 32-bit)
     return norm_call<false>(dtype, a, stream);
 }
