@@ -40,7 +40,7 @@ struct Args {
     int split;                           // blocks of a cluster, along K
     int tiles_x, tiles_y;                // tiles of the 128-row operand, of the other
     int out_dtype;
-    int vec;                             // out rows are 16-byte aligned
+    int vec;                             // every fourth column of out is aligned for four
 };
 
 constexpr int kXBytes = 128 * 128;
@@ -54,36 +54,30 @@ template <int NT, bool SWAP, int CPS> struct Conf {
     static constexpr int nst = kRing / stage;
     static constexpr int nbuf = NT > 128 ? 2 : 4;                     // TMEM buffers
     static constexpr int cols = nbuf * NT;                            // a power of two, >= 32
-    static constexpr int scales = SWAP ? 2 * 4 * NT * 4 : 0;          // two groups of four k-blocks' column scales
+    static constexpr int scales = 2 * 4 * (SWAP ? NT : EW * 32) * 4;  // two groups of four k-blocks' scales
+    // the output tile on its way out, [token row][weight row] in fp32 in place of the ring
+    static constexpr int lines = SWAP ? NT : 128, len = SWAP ? 128 : NT, pitch = SWAP ? 128 : NT + 4;
     // barriers: stage full / empty, buffer full / empty, drain
     static constexpr int bars = nst * stage;
     static constexpr int nbars = 2 * nst + 2 * nbuf + 1;
     static constexpr int svec = (bars + nbars * 8 + 16 + 15) & ~15;
     static constexpr int total = svec + scales + 1024;
-    static_assert(nst >= 2 && NT * 512 <= nst * stage, "ring");
+    static_assert(nst >= 2 && lines * pitch * 4 <= nst * stage, "ring");
 };
 
-template <typename T> __device__ __forceinline__ void put(void *out, size_t i, float v)
+// Four consecutive columns of one row, the first n of them inside the matrix.
+template <typename T> __device__ __forceinline__ void put4(T *out, float4 x, int n, bool vec)
 {
-    static_cast<T *>(out)[i] = from_f32<T>(v);
-}
-__device__ __forceinline__ void put_any(int dtype, void *out, size_t i, float v)
-{
-    if (dtype == ORTHRUS_BF16) put<__nv_bfloat16>(out, i, v);
-    else if (dtype == ORTHRUS_F16) put<__half>(out, i, v);
-    else put<float>(out, i, v);
-}
-// eight consecutive columns of one row, the first n of them inside the matrix
-__device__ __forceinline__ void put8(const Args &p, size_t at, const float (&x)[8], int n)
-{
-    if (p.vec && n >= 8) {
-        if (p.out_dtype == ORTHRUS_BF16) store8(static_cast<__nv_bfloat16 *>(p.out) + at, x);
-        else if (p.out_dtype == ORTHRUS_F16) store8(static_cast<__half *>(p.out) + at, x);
-        else store8(static_cast<float *>(p.out) + at, x);
+    if (vec && n >= 4) {
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(x.x, x.y), pack2<T>(x.z, x.w));
+        else
+            *reinterpret_cast<float4 *>(out) = x;
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) put_any(p.out_dtype, p.out, at + j, x[j]);
+        if (n > 0) out[0] = from_f32<T>(x.x);
+        if (n > 1) out[1] = from_f32<T>(x.y);
+        if (n > 2) out[2] = from_f32<T>(x.z);
+        if (n > 3) out[3] = from_f32<T>(x.w);
     }
 }
 
@@ -146,80 +140,63 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
         const int half = warp >> 2;                                   // which CPT columns
         const int row = (warp & 3) * 32 + lane;
         const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * C::CPT;
-        // scales of a group of four k-blocks, fetched one group ahead
+        // scales of a group of four k-blocks, fetched one group ahead: of the
+        // thread's own row, or (SWAP) of the columns, shared by the four warps.
+        // They go through shared memory in both forms so that the loop over
+        // k-blocks is one small body: unrolled over a group it drove the
+        // producer's and the MMA warp's code out of the instruction cache, and
+        // each of their steps took ~350 cycles.
+        constexpr int NS = SWAP ? NT : C::EW * 32;
+        float *svec = reinterpret_cast<float *>(sm + C::svec);        // [2][4][NS]
         float next[4];
-        const bool mine = SWAP ? (int)threadIdx.x < NT && y0 + (int)threadIdx.x < p.M : x0 + row < p.M;
-        const float *sa = p.a_scale + (size_t)(SWAP ? y0 + (int)threadIdx.x : x0 + row) * p.nkb;
-        const float *sw = p.w_scale + (size_t)(SWAP ? tx : (y0 + half * 128) / 128) * p.nkb;
-        const bool sw_in = SWAP || y0 + half * 128 < p.N;
+        const int sr = SWAP ? y0 + (int)threadIdx.x : x0 + row;
+        const bool mine = sr < p.M && (SWAP ? (int)threadIdx.x < NT : y0 + half * 128 < p.N);
+        const float *sa = p.a_scale + (size_t)(mine ? sr : 0) * p.nkb;
+        const float *sw = p.w_scale + (size_t)(SWAP ? tx : mine ? (y0 + half * 128) / 128 : 0) * p.nkb;
         auto fetch = [&](int k) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                next[j] = mine && sw_in && k + j < k_hi ? __ldg(sa + k + j) * __ldg(sw + k + j) : 0.f;
+            for (int j = 0; j < 4; ++j) next[j] = mine && k + j < k_hi ? __ldg(sa + k + j) * __ldg(sw + k + j) : 0.f;
         };
-        float *svec = reinterpret_cast<float *>(sm + C::svec);        // [2][4][NT]
         fetch(k_lo);
-        for (int i = 0; i < nk; i += 4) {          // (after an abort too: the warps meet at barrier 1)
-            float cur[4];
+#pragma unroll 1
+        for (int it = 0; it < nk; ++it) {
+            if ((it & 3) == 0) {                   // (after an abort too: the warps meet at barrier 1)
+                float *sv = svec + ((it >> 2) & 1) * 4 * NS;
+                if (!SWAP || (int)threadIdx.x < NT) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cur[j] = next[j];
-            float *sv = svec + ((i >> 2) & 1) * 4 * NT;
-            if (SWAP) {
-                if ((int)threadIdx.x < NT) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sv[j * NT + threadIdx.x] = cur[j];
+                    for (int j = 0; j < 4; ++j) sv[j * NS + threadIdx.x] = next[j];
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (SWAP) asm volatile("bar.sync 1, 128;" ::: "memory");
+                fetch(k_lo + it + 4);
             }
-            if (i + 4 < nk) fetch(k_lo + i + 4);
+            if (!ok) continue;
+            const float *sv = svec + (it & 7) * NS;
+            const float own_scale = SWAP ? 0.f : sv[threadIdx.x];
+            const int buf = it % C::nbuf;
+            ok = __all_sync(~0u, wait_bar_near(b_tfull + 8 * buf, (it / C::nbuf) & 1, abort_flag, p.status));
+            if (!ok) continue;
+            tc_fence_after();
+            constexpr int W = C::CPT < 32 ? 16 : 32;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (i + j >= nk || !ok) break;
-                const int it = i + j, buf = it % C::nbuf;
-                ok = __all_sync(~0u, wait_bar(b_tfull + 8 * buf, (it / C::nbuf) & 1, abort_flag, p.status));
-                if (!ok) break;
-                tc_fence_after();
-                constexpr int W = C::CPT < 32 ? 16 : 32;
+            for (int c = 0; c < C::CPT; c += W) {
+                uint32_t v[W];
+                if constexpr (W == 32) tmem_ld32(t_row + buf * NT + c, v);
+                else tmem_ld16(t_row + buf * NT + c, v);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < C::CPT; c += W) {
-                    uint32_t v[W];
-                    if constexpr (W == 32) tmem_ld32(t_row + buf * NT + c, v);
-                    else tmem_ld16(t_row + buf * NT + c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q = 0; q < W; q += 4) {
-                        const float4 s = SWAP ? *reinterpret_cast<const float4 *>(sv + j * NT + c + q)
-                                              : make_float4(cur[j], cur[j], cur[j], cur[j]);
-                        const float2 u = ffma2(make_float2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])),
-                                               make_float2(s.x, s.y), make_float2(acc[c + q], acc[c + q + 1]));
-                        const float2 w = ffma2(make_float2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])),
-                                               make_float2(s.z, s.w), make_float2(acc[c + q + 2], acc[c + q + 3]));
-                        acc[c + q] = u.x, acc[c + q + 1] = u.y, acc[c + q + 2] = w.x, acc[c + q + 3] = w.y;
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_tempty + 8 * buf);
-            }
-        }
-        if (p.split == 1 && ok) {
-            if (SWAP) {
-                const int n = x0 + row;
-                if (n < p.N) {
-#pragma unroll
-                    for (int c = 0; c < C::CPT; ++c)
-                        if (y0 + c < p.M) put_any(p.out_dtype, p.out, (size_t)(y0 + c) * p.N + n, acc[c]);
-                }
-            } else if (x0 + row < p.M) {
-                const int n0 = y0 + half * C::CPT;
-#pragma unroll
-                for (int c = 0; c < C::CPT; c += 8) {
-                    float x[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = acc[c + j];
-                    put8(p, (size_t)(x0 + row) * p.N + n0 + c, x, p.N - n0 - c);
+                for (int q = 0; q < W; q += 4) {
+                    const float4 s = SWAP ? *reinterpret_cast<const float4 *>(sv + c + q)
+                                          : make_float4(own_scale, own_scale, own_scale, own_scale);
+                    const float2 u = ffma2(make_float2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])),
+                                           make_float2(s.x, s.y), make_float2(acc[c + q], acc[c + q + 1]));
+                    const float2 w = ffma2(make_float2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])),
+                                           make_float2(s.z, s.w), make_float2(acc[c + q + 2], acc[c + q + 3]));
+                    acc[c + q] = u.x, acc[c + q + 1] = u.y, acc[c + q + 2] = w.x, acc[c + q + 3] = w.y;
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_tempty + 8 * buf);
         }
     } else if (warp == C::EW) {
         if (lane == 0) {
@@ -229,7 +206,7 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
             int it = 0;
             for (; it < ns; ++it) {
                 const int st = it % C::nst, n = it / C::nst;
-                if (n > 0 && !wait_bar(b_empty + 8 * st, (n - 1) & 1, abort_flag, p.status)) {
+                if (n > 0 && !wait_bar_near(b_empty + 8 * st, (n - 1) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
@@ -256,14 +233,14 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
             const int ns = (nk + CPS - 1) / CPS;
             for (int it = 0; it < ns && ok; ++it) {
                 const int st = it % C::nst;
-                if (!wait_bar(b_full + 8 * st, (it / C::nst) & 1, abort_flag, p.status)) {
+                if (!wait_bar_near(b_full + 8 * st, (it / C::nst) & 1, abort_flag, p.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 for (int j = 0; j < CPS && it * CPS + j < nk; ++j) {
                     const int kb = it * CPS + j, buf = kb % C::nbuf, n = kb / C::nbuf;
-                    if (n > 0 && !wait_bar(b_tempty + 8 * buf, (n - 1) & 1, abort_flag, p.status)) {
+                    if (n > 0 && !wait_bar_near(b_tempty + 8 * buf, (n - 1) & 1, abort_flag, p.status)) {
                         ok = false;
                         break;
                     }
@@ -285,43 +262,51 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
         __syncwarp();
     }
 
-    if (p.split > 1) {
-        // partials to shared memory ([column][row], in the ring: every load has
-        // been consumed), then each rank adds its share of the columns over the
-        // ranks, in rank order
-        float *part = reinterpret_cast<float *>(sm);
+    // ---- output: the tile goes through shared memory (the ring: every load has
+    // been consumed) so that the stores are whole rows of it; with a split each
+    // rank writes its share of the token rows, added over the ranks in order.
+    float *tile_o = reinterpret_cast<float *>(sm);
+    __syncthreads();
+    if (warp < C::EW) {
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-        __syncthreads();
-        if (warp < C::EW) {
+        if (SWAP) {
 #pragma unroll
-            for (int c = 0; c < C::CPT; ++c) part[(half * C::CPT + c) * 128 + row] = acc[c];
+            for (int c = 0; c < C::CPT; ++c) tile_o[c * C::pitch + row] = acc[c];
+        } else {
+#pragma unroll
+            for (int c = 0; c < C::CPT; c += 4)
+                *reinterpret_cast<float4 *>(tile_o + row * C::pitch + half * C::CPT + c) =
+                    make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
         }
-        cluster_sync();
-        if (warp < C::EW && !*abort_flag) {
-            const int groups = NT / 8;                                // shares of whole groups of eight columns
-            const int g_lo = rank * groups / p.split, g_hi = (rank + 1) * groups / p.split;
-            for (int g = g_lo + half; g < g_hi; g += C::EW / 4) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = 0.f;
-                for (int r = 0; r < p.split; ++r) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        x[j] += ld_cluster_f32(base + (uint32_t)((g * 8 + j) * 128 + row) * 4u, r);
-                }
-                if (SWAP) {
-                    const int n = x0 + row;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (n < p.N && y0 + g * 8 + j < p.M)
-                            put_any(p.out_dtype, p.out, (size_t)(y0 + g * 8 + j) * p.N + n, x[j]);
-                } else if (x0 + row < p.M) {
-                    put8(p, (size_t)(x0 + row) * p.N + y0 + g * 8, x, p.N - y0 - g * 8);
-                }
-            }
-        }
-        cluster_sync();                                               // no block leaves while its partials are read
     }
+    if (p.split > 1) cluster_sync();
+    else __syncthreads();
+    const int m0 = SWAP ? y0 : x0, n0 = SWAP ? x0 : y0;
+    if (!*abort_flag) {
+        constexpr int per = C::len / 4;                               // threads of a token row
+#pragma unroll 1
+        for (int i = threadIdx.x; i < C::lines * per; i += C::threads) {
+            const int line = i / per, e = (i % per) * 4;
+            const int m = m0 + line, n = n0 + e;
+            if (m >= p.M || n >= p.N || (p.split > 1 && line % p.split != rank)) continue;
+            float4 x;
+            if (p.split > 1) {
+                x = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint32_t at = base + (uint32_t)(line * C::pitch + e) * 4u;
+                for (int r = 0; r < p.split; ++r) {
+                    const float4 v = ld_cluster_f32x4(at, r);
+                    x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+                }
+            } else {
+                x = *reinterpret_cast<const float4 *>(tile_o + line * C::pitch + e);
+            }
+            const size_t at = (size_t)m * p.N + n;
+            if (p.out_dtype == ORTHRUS_BF16) put4(static_cast<__nv_bfloat16 *>(p.out) + at, x, p.N - n, p.vec);
+            else if (p.out_dtype == ORTHRUS_F16) put4(static_cast<__half *>(p.out) + at, x, p.N - n, p.vec);
+            else put4(static_cast<float *>(p.out) + at, x, p.N - n, p.vec);
+        }
+    }
+    if (p.split > 1) cluster_sync();                                  // no block leaves while its partials are read
     tc_fence_before();
     __syncthreads();
     if (warp == C::EW + 1) {
@@ -329,6 +314,14 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::cols) : "memory");
     }
 }
+
+}  // namespace f8
+}  // namespace orthrus
+
+#include "fp8_pair.cuh"
+
+namespace orthrus {
+namespace f8 {
 
 constexpr int kMaxDevices = 64;
 
@@ -385,6 +378,67 @@ int launch(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t
     return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
 }
 
+template <typename T> bool pair_ready(int dev)
+{
+    static std::once_flag once[kMaxDevices];
+    static bool ok[kMaxDevices];
+    if (dev < 0 || dev >= kMaxDevices) return false;
+    std::call_once(once[dev], [dev] {
+        ok[dev] = cudaFuncSetAttribute(fp8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       PairConf::total) == cudaSuccess;
+        if (!ok[dev]) cudaGetLastError();
+    });
+    return ok[dev];
+}
+
+template <typename T>
+int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t st)
+{
+    using C = PairConf;
+    p.tiles_x = (p.M + 255) / 256;
+    p.tiles_y = (p.N + kPairN - 1) / kPairN;
+    const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
+    if (tiles >= 1ll << 28) return ORTHRUS_ERR_UNSUPPORTED;
+    p.vec = ((uintptr_t)p.out & 15u) == 0 && (int64_t)p.N * (int)sizeof(T) % 16 == 0 &&
+            (int64_t)p.N * (int)sizeof(T) < 1ll << 31;
+    PairMaps mp;
+    const uint64_t str[1] = {(uint64_t)p.K}, ostr[1] = {(uint64_t)p.N * sizeof(T)};
+    const uint64_t dx[2] = {(uint64_t)p.K, (uint64_t)p.M}, dy[2] = {(uint64_t)p.K, (uint64_t)p.N},
+                   dz[2] = {(uint64_t)p.N * sizeof(T), (uint64_t)p.M};
+    const uint32_t bx[2] = {128, 128}, by[2] = {128, 64};
+    if (!encode_u8_sw128(&mp.x, 2, a, dx, str, bx) || !encode_u8_sw128(&mp.y, 2, w, dy, str, by)) return ORTHRUS_ERR_LAUNCH;
+    if (p.vec) {
+        if (!encode_u8_sw128(&mp.o, 2, p.out, dz, ostr, bx)) return ORTHRUS_ERR_LAUNCH;
+    } else {
+        mp.o = mp.x;                                                  // (not used)
+    }
+    if (!pair_ready<T>(dev)) return ORTHRUS_ERR_LAUNCH;
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = C::total;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T>, mp, p);
+    return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
+}
+
+int launch_pair(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t st)
+{
+    return p.out_dtype == ORTHRUS_BF16  ? launch_pair_t<__nv_bfloat16>(p, a, w, dev, sms, st)
+           : p.out_dtype == ORTHRUS_F16 ? launch_pair_t<__half>(p, a, w, dev, sms, st)
+                                        : launch_pair_t<float>(p, a, w, dev, sms, st);
+}
+
 }  // namespace f8
 
 }  // namespace orthrus
@@ -415,11 +469,11 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     p.K = K;
     p.nkb = (K + ORTHRUS_FP8_BLOCK - 1) / ORTHRUS_FP8_BLOCK;
     p.out_dtype = out_dtype;
-    p.vec = ((uintptr_t)out & 15u) == 0 && (int64_t)N * e % 16 == 0;
+    p.vec = ((uintptr_t)out & (uintptr_t)(4 * e - 1)) == 0 && N % 4 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (M <= 16) return f8::launch<16, true, 4>(p, a, w, dev, sms, st);
     if (M <= 32) return f8::launch<32, true, 4>(p, a, w, dev, sms, st);
     if (M <= 64) return f8::launch<64, true, 2>(p, a, w, dev, sms, st);
     if (M <= 128) return f8::launch<128, true, 2>(p, a, w, dev, sms, st);
-    return f8::launch<256, false, 1>(p, a, w, dev, sms, st);
+    return f8::launch_pair(p, a, w, dev, sms, st);
 }

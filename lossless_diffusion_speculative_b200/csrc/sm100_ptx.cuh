@@ -90,6 +90,13 @@ static __device__ __noinline__ bool wait_bar(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// The same with its first test inline: where the phase is usually complete, the
+// wait stays within the caller's own instructions.
+__device__ __forceinline__ bool wait_bar_near(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+{
+    return mbar_try(bar, parity) || wait_bar(bar, parity, abort_flag, status);
+}
+
 // Drain wait used on the abort path: bounded, no side effects.
 static __device__ __noinline__ void wait_bar_quiet(uint32_t bar, uint32_t parity)
 {
@@ -313,6 +320,81 @@ __device__ __forceinline__ void pdl_trigger()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// One lane of a converged warp; code under it keeps warp-uniform operands.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// ---- pairs of CTAs (cta_group::2, a cluster of two).  Both CTAs hold their half
+// of the operands at the same shared-memory offsets; the even CTA issues.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t own_addr, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(own_addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Load into this CTA's shared memory, counted on a barrier of the pair's even CTA.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *m, uint32_t cluster_bar, int x, int y,
+                                                 uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"((unsigned long long)m), "r"(cluster_bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs (or, `own`, in this one)
+// when the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_own(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Tiled copy of a box from shared to global memory, in the issuing thread's
+// bulk-async group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, uint32_t src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     (unsigned long long)m),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// Asynchronous copies of 16 (4) bytes into shared memory; zeros where not `full`.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool full)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool full)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(full ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Bulk copy of `bytes` (multiple of 16) from this CTA's shared memory to
 // global memory, tracked by the issuing thread's bulk-async group.
 __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes)
@@ -389,16 +471,17 @@ __host__ __device__ constexpr uint32_t instr_desc_e4m3(int M, int N)
 }
 
 // Thread-block clusters: every thread of every block arrives, then waits; and
-// a float of another block's shared memory at the address of an own one.
+// four floats of another block's shared memory at the address of own ones.
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t own_addr, uint32_t rank)
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t own_addr, uint32_t rank)
 {
-    float v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                 : "=f"(v)
+    float4 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+                 "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                  : "r"(own_addr), "r"(rank)
                  : "memory");
     return v;
