@@ -28,7 +28,7 @@ constexpr int kScaleGroup = 16;                       // k-blocks whose scales a
 constexpr int kScalePitch = 129;                      // row scales [k-block][row], padded for the copies' banks
 
 struct PairMaps {
-    CUtensorMap x, y, o;                 // a: box 128 x 128; w: box 128 x 64; out: box 128 bytes x 128 rows
+    CUtensorMap x, y, o;                 // a: box 128 x 128; w: box 128 x 128; out: box 128 bytes x 128 rows
 };
 
 struct PairConf {
@@ -37,12 +37,12 @@ struct PairConf {
     static constexpr int out_half = 32 * 1024;                        // staging of one column half: two boxes
     static constexpr int out = nst * stage;
     static constexpr int bars = out + 2 * out_half;
-    // stage full / empty, TMEM buffer [half][2] full / empty, scale group full / empty, drain
-    static constexpr int nbars = 2 * nst + 8 + 4 + 1;
+    // stage full / empty, TMEM buffer full / empty, scale group full / empty, drain
+    static constexpr int nbars = 2 * nst + 4 + 4 + 1;
     static constexpr int sa = (bars + nbars * 8 + 16 + 15) & ~15;     // [2][16][129] row scales
     static constexpr int sw = sa + 2 * kScaleGroup * kScalePitch * 4; // [2][2 halves][16] weight scales
     static constexpr int total = sw + 2 * 2 * kScaleGroup * 4 + 1024;
-    static_assert(total <= 227 * 1024, "shared memory");
+    static_assert(total <= 227 * 1024 && nst == 4, "shared memory; the MMA loop's parities");
 };
 
 // Token tiles first, in strips of 8 tiles, so that the tiles in flight share operands in L2.
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sm = smem_raw + (base - raw);
     const uint32_t b_full = base + C::bars, b_empty = b_full + 8 * C::nst, b_tfull = b_empty + 8 * C::nst,
-                   b_tempty = b_tfull + 32, b_sfull = b_tempty + 32, b_sempty = b_sfull + 16, b_drain = b_sempty + 16;
+                   b_tempty = b_tfull + 16, b_sfull = b_tempty + 16, b_sempty = b_sfull + 16, b_drain = b_sempty + 16;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::bars + C::nbars * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -93,11 +93,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(b_tfull + 8 * i, 1);
-            mbar_init(b_tempty + 8 * i, kEpiWarps);                   // four warps of both CTAs
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(b_tfull + 8 * i, 1);
+            mbar_init(b_tempty + 8 * i, 2 * kEpiWarps);               // the warps of both CTAs
             mbar_init(b_sfull + 8 * i, 1);
             mbar_init(b_sempty + 8 * i, kEpiWarps);
         }
@@ -127,8 +125,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     if (warp < kEpiWarps) {
         constexpr int CPT = kPairN / 2;
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 2 * CPT;
-        const uint32_t tfull = b_tfull + 16 * half, lead_tempty = map_to_rank(b_tempty + 16 * half, 0);
+        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * CPT;
+        const uint32_t lead_tempty = map_to_rank(b_tempty, 0);
         const float *sa = reinterpret_cast<const float *>(sm + C::sa) + row;
         const float *sw = reinterpret_cast<const float *>(sm + C::sw) + half * kScaleGroup;
         // staging of this half: boxes of 128 rows x 128 bytes, 16-byte chunks swizzled by the row
@@ -153,17 +151,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                 if (!ok) continue;
                 const float sc = sa[(gb * kScaleGroup + in) * kScalePitch] * sw[gb * 2 * kScaleGroup + in];
                 const float2 s2 = make_float2(sc, sc);
-                ok = __all_sync(~0u, wait_bar_near(tfull + 8 * buf, (it >> 1) & 1, abort_flag, p.status));
+                ok = __all_sync(~0u, wait_bar_near(b_tfull + 8 * buf, (it >> 1) & 1, abort_flag, p.status));
                 if (!ok) continue;
                 tc_fence_after();
                 // two chunks of 16 columns: one on its way while the other is added
                 uint32_t v[2][16];
-                tmem_ld16(t_row + buf * CPT, v[0]);
+                tmem_ld16(t_row + buf * kPairN, v[0]);
 #pragma unroll
                 for (int c = 0; c < CPT; c += 16) {
                     tmem_wait_ld();
                     if (c + 16 < CPT) {
-                        tmem_ld16(t_row + buf * CPT + c + 16, v[(c / 16 + 1) & 1]);
+                        tmem_ld16(t_row + buf * kPairN + c + 16, v[(c / 16 + 1) & 1]);
                     } else {                                          // all read: the buffer is free
                         tc_fence_before();
                         __syncwarp();
@@ -234,71 +232,62 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
         if ((threadIdx.x & 127) == 0) bulk_wait_all();
     } else if (warp == kEpiWarps) {
         // ---- producer: this CTA's token rows, and its 64 weight rows of either column half
-        const uint64_t keep = make_policy_evict_last();
-        const bool lead = elect_one();
-        int it = 0;
-        bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
-            int x, y;
-            pair_tile(p, t, x, y);
-            const int m0 = x * 256 + rank * 128, n0 = y * kPairN + rank * 64;
+        if (elect_one()) {
+            const uint64_t keep = make_policy_evict_last();
+            int it = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int x, y;
+                pair_tile(p, t, x, y);
+                const int m0 = x * 256 + rank * 128, n0 = y * kPairN + rank * 128;
 #pragma unroll 1
-            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const int st = it % C::nst, n = it / C::nst;
-                if (n > 0) ok = __all_sync(~0u, wait_bar_near(b_empty + 8 * st, (n - 1) & 1, abort_flag, p.status));
-                if (!ok) break;
-                if (lead) {
+                for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+                    const int st = it % C::nst, n = it / C::nst;
+                    if (n > 0) ok = wait_bar_near(b_empty + 8 * st, (n - 1) & 1, abort_flag, p.status);
+                    if (!ok) break;
                     const uint32_t full = map_to_rank(b_full + 8 * st, 0), dst = base + st * C::stage;
                     if (rank == 0) mbar_expect_tx(b_full + 8 * st, 2 * C::stage);
                     tma_load_2d_pair(dst, &mp.x, full, kb * 128, m0, keep);
                     tma_load_2d_pair(dst + kXBytes, &mp.y, full, kb * 128, n0, keep);
-                    tma_load_2d_pair(dst + kXBytes + 8192, &mp.y, full, kb * 128, n0 + 128, keep);
                 }
-                __syncwarp();
             }
-        }
-        if (!ok && rank == 0 && lead) {                               // abort: let both CTAs' copies in flight land
-            for (int st = 0; st < C::nst; ++st) {
-                const int fills = it / C::nst + (st < it % C::nst ? 1 : 0);
-                if (fills) wait_bar_quiet(b_full + 8 * st, (fills - 1) & 1);
+            if (!ok && rank == 0) {                                   // abort: let both CTAs' copies in flight land
+                for (int st = 0; st < C::nst; ++st) {
+                    const int fills = it / C::nst + (st < it % C::nst ? 1 : 0);
+                    if (fills) wait_bar_quiet(b_full + 8 * st, (fills - 1) & 1);
+                }
             }
         }
         __syncwarp();
     } else if (warp == kEpiWarps + 1) {
-        // ---- MMA: the even CTA issues for both, a column half at a time
-        constexpr uint32_t idesc = instr_desc_e4m3(256, kPairN / 2);
-        const bool lead = elect_one();
-        int it = 0;
-        bool ok = true;
-        for (int t = pair; rank == 0 && t < tiles && ok; t += pairs) {
+        // ---- MMA: the even CTA issues for both
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = instr_desc_e4m3(256, kPairN);
+            const int steps = (tiles - pair + pairs - 1) / pairs * p.nkb;
+            const uint64_t ax0 = smem_desc(base, 16, 1024), ay0 = smem_desc(base + kXBytes, 16, 1024);
+            bool ok = true;
+            uint32_t par = 0;                                         // parity of the stage ring's round
 #pragma unroll 1
-            for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-                const int st = it % C::nst, buf = it & 1, n = it >> 1;
-                ok = __all_sync(~0u, wait_bar_near(b_full + 8 * st, (it / C::nst) & 1, abort_flag, p.status));
-                if (!ok) break;
-                const uint32_t dst = base + st * C::stage;
-                const uint64_t ax = smem_desc(dst, 16, 1024);
+            for (int it = 0; ok && it < steps; it += C::nst, par ^= 1) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (ok && n > 0)
-                        ok = __all_sync(~0u, wait_bar_near(b_tempty + 16 * h + 8 * buf, (n - 1) & 1, abort_flag, p.status));
+                for (int st = 0; st < C::nst; ++st) {                 // (nst is even: buffer st & 1, used twice a round)
+                    if (it + st >= steps) break;
+                    ok = (it + st < 2 || wait_bar_near(b_tempty + 8 * (st & 1), ((st >> 1) & 1) ^ 1, abort_flag, p.status)) &&
+                         wait_bar_near(b_full + 8 * st, par, abort_flag, p.status);
+                    if (!ok) break;
                     tc_fence_after();
-                    if (ok && lead) {
-                        const uint64_t ay = smem_desc(dst + kXBytes + h * 8192, 16, 1024);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            tc_mma_f8_pair(tmem + (h * 2 + buf) * (kPairN / 2), ax + 2 * q, ay + 2 * q, idesc, q);
-                        tc_commit_pair(b_tfull + 16 * h + 8 * buf);
-                        if (h == 1) tc_commit_pair(b_empty + 8 * st);
-                    }
-                    __syncwarp();
+                    for (int q = 0; q < 4; ++q)
+                        tc_mma_f8_pair(tmem + (st & 1) * kPairN, ax0 + st * (C::stage >> 4) + 2 * q,
+                                       ay0 + st * (C::stage >> 4) + 2 * q, idesc, q);
+                    tc_commit_pair(b_tfull + 8 * (st & 1));
+                    tc_commit_pair(b_empty + 8 * st);
                 }
-                if (!ok) break;
             }
-        }
-        if (!ok && lead) {
-            tc_commit_pair_own(b_drain);
-            wait_bar_quiet(b_drain, 0);
+            if (!ok) {
+                tc_commit_pair_own(b_drain);
+                wait_bar_quiet(b_drain, 0);
+            }
         }
         __syncwarp();
     } else {
