@@ -9,18 +9,28 @@
 // registers while the next blocks are multiplied.  (The sum of a block is exact
 // to fp32 in the tensor cores.)
 //
-// Two forms of one kernel.  SWAP (few token rows): the weight rows are the
-// MMA's 128 rows and up to 128 token rows its columns, so that no part of the
-// MMA is padding and the weights are streamed once; bound by HBM.  Otherwise a
-// thread owns a token row of a 128 x NT tile; bound by the tensor cores.  A K
-// split over a cluster of blocks (partials joined through distributed shared
-// memory, in rank order) fills the SMs where there are few tiles.
+// Few token rows (this file): the weight rows are the MMA's 128 rows and up to
+// 128 token rows its columns, so that no part of the MMA is padding and the
+// weights are streamed once; bound by HBM.  The weight rows are cut into ranges
+// of 16-row granules, one per block, walked in tiles of up to 128 rows with the
+// loads running ahead across tiles.  Where whole tiles are too few for the SMs
+// a K split over a cluster of blocks (partials joined through distributed
+// shared memory, in rank order) fills them.  The steps of the pipeline are
+// groups of GRP k-blocks: every wait, signal and issue of a step costs 50-150
+// cycles of latency, which per single block (530 cycles a block measured, 16 KB
+// of weights) was more than the SM's share of HBM takes to deliver it.
+// Many token rows: fp8_pair.cuh.
 //
-// Roles: warps 0..EW-1 epilogue, then a TMA producer warp and an MMA warp.
+// Roles: warps 0..3 epilogue, then a TMA producer warp and an MMA warp (one
+// elected thread each).
 #include <mutex>
 
 #include "kernels.h"
 #include "layer_ops.cuh"
+
+#ifndef ORTHRUS_FORCE_ROWS
+#define ORTHRUS_FORCE_ROWS 0
+#endif
 
 namespace orthrus {
 
@@ -29,7 +39,7 @@ namespace f8 {
 using namespace sm100;
 
 struct Maps {
-    CUtensorMap x, y;                    // 128-row operand (box 128 x 128), NT-row operand (box 128 x NT)
+    CUtensorMap w, w16, a;               // weights: box 128 x 128 and 128 x 16 rows; tokens: box 128 x NT
 };
 
 struct Args {
@@ -38,31 +48,25 @@ struct Args {
     int32_t *status;
     int M, N, K, nkb;
     int split;                           // blocks of a cluster, along K
-    int tiles_x, tiles_y;                // tiles of the 128-row operand, of the other
+    int tiles_x, tiles_y;                // tiles of the weight (pair: token) rows, of the others
+    int ranges;                          // split == 1: blocks that share the weight rows of one token tile
     int out_dtype;
-    int vec;                             // every fourth column of out is aligned for four
+    int vec;                             // every fourth column of out (pair: every row) is aligned
 };
 
 constexpr int kXBytes = 128 * 128;
-constexpr int kRing = 192 * 1024;
 
-template <int NT, bool SWAP, int CPS> struct Conf {
-    static constexpr int EW = NT > 128 ? 8 : 4;                       // epilogue warps
-    static constexpr int CPT = NT > 128 ? NT / 2 : NT;                // columns of a thread
-    static constexpr int threads = (EW + 2) * 32;
-    static constexpr int stage = CPS * (kXBytes + NT * 128);
-    static constexpr int nst = kRing / stage;
-    static constexpr int nbuf = NT > 128 ? 2 : 4;                     // TMEM buffers
-    static constexpr int cols = nbuf * NT;                            // a power of two, >= 32
-    static constexpr int scales = 2 * 4 * (SWAP ? NT : EW * 32) * 4;  // two groups of four k-blocks' scales
-    // the output tile on its way out, [token row][weight row] in fp32 in place of the ring
-    static constexpr int lines = SWAP ? NT : 128, len = SWAP ? 128 : NT, pitch = SWAP ? 128 : NT + 4;
-    // barriers: stage full / empty, buffer full / empty, drain
-    static constexpr int bars = nst * stage;
-    static constexpr int nbars = 2 * nst + 2 * nbuf + 1;
-    static constexpr int svec = (bars + nbars * 8 + 16 + 15) & ~15;
-    static constexpr int total = svec + scales + 1024;
-    static_assert(nst >= 2 && lines * pitch * 4 <= nst * stage, "ring");
+template <int NT, int GRP, int NST> struct Conf {
+    static constexpr int threads = 6 * 32;
+    static constexpr int stage = GRP * (kXBytes + NT * 128);
+    static constexpr int cols = 2 * GRP * NT;                         // two sets of GRP buffers; a power of two
+    static constexpr int tile = NST * stage;                          // the output tile, [token][weight row] in fp32
+    static constexpr int bars = tile + NT * 128 * 4;
+    static constexpr int nbars = 2 * NST + 4 + 1;                     // stage full / empty, set full / empty, drain
+    static constexpr int svec = (bars + nbars * 8 + 16 + 15) & ~15;   // [2][2 weight blocks][GRP][NT] scales
+    static constexpr int total = svec + 2 * 2 * GRP * NT * 4 + 1024;
+    static_assert(cols >= 32 && cols <= 512 && (cols & (cols - 1)) == 0, "TMEM");
+    static_assert(total <= 227 * 1024, "shared memory");
 };
 
 // Four consecutive columns of one row, the first n of them inside the matrix.
@@ -80,39 +84,46 @@ template <typename T> __device__ __forceinline__ void put4(T *out, float4 x, int
         if (n > 3) out[3] = from_f32<T>(x.w);
     }
 }
-
-template <int NT, bool SWAP, int CPS>
-__global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
-    fp8_matmul_kernel(const __grid_constant__ Maps mp, const Args p)
+__device__ __forceinline__ void put4_any(const Args &p, size_t at, float4 x, int n)
 {
-    using C = Conf<NT, SWAP, CPS>;
+    if (p.out_dtype == ORTHRUS_BF16) put4(static_cast<__nv_bfloat16 *>(p.out) + at, x, n, p.vec);
+    else if (p.out_dtype == ORTHRUS_F16) put4(static_cast<__half *>(p.out) + at, x, n, p.vec);
+    else put4(static_cast<float *>(p.out) + at, x, n, p.vec);
+}
+
+template <int NT, int GRP, int NST>
+__global__ void __launch_bounds__(Conf<NT, GRP, NST>::threads, 1)
+    fp8_rows_kernel(const __grid_constant__ Maps mp, const Args p)
+{
+    using C = Conf<NT, GRP, NST>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sm = smem_raw + (base - raw);
-    const uint32_t b_full = base + C::bars, b_empty = b_full + 8 * C::nst, b_tfull = b_empty + 8 * C::nst,
-                   b_tempty = b_tfull + 8 * C::nbuf, b_drain = b_tempty + 8 * C::nbuf;
+    const uint32_t b_full = base + C::bars, b_empty = b_full + 8 * NST, b_tfull = b_empty + 8 * NST,
+                   b_tempty = b_tfull + 16, b_drain = b_tempty + 16;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::bars + C::nbars * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::nst; ++i) {
+        for (int i = 0; i < NST; ++i) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 1);
         }
-        for (int i = 0; i < C::nbuf; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(b_tfull + 8 * i, 1);
-            mbar_init(b_tempty + 8 * i, C::EW);
+            mbar_init(b_tempty + 8 * i, 4);
         }
         mbar_init(b_drain, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == C::EW && lane == 0) {
-        tma_prefetch(&mp.x);
-        tma_prefetch(&mp.y);
+    if (warp == 4 && lane == 0) {
+        tma_prefetch(&mp.w);
+        tma_prefetch(&mp.w16);
+        tma_prefetch(&mp.a);
     }
-    if (warp == C::EW + 1) {
+    if (warp == 5) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + C::bars +
                                                                                                C::nbars * 8),
                      "r"(C::cols)
@@ -124,135 +135,181 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
     tc_fence_after();
     const uint32_t tmem = misc[0];
 
-    const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
-    const int tx = tile % p.tiles_x, ty = tile / p.tiles_x;
-    const int x0 = tx * 128, y0 = ty * NT;
+    // this block's weight rows [r_lo, r_hi), token rows from y0, k-blocks [k_lo, k_hi)
+    int rank = 0, y0, r_lo, r_hi;
+    if (p.split > 1) {
+        rank = blockIdx.x % p.split;
+        const int t = blockIdx.x / p.split;
+        y0 = t / p.tiles_x * NT;
+        r_lo = t % p.tiles_x * 128;
+        r_hi = r_lo + 128;
+    } else {
+        const int g16 = (p.N + 15) >> 4, c = blockIdx.x % p.ranges;
+        y0 = blockIdx.x / p.ranges * NT;
+        r_lo = 16 * (int)((int64_t)c * g16 / p.ranges);
+        r_hi = 16 * (int)((int64_t)(c + 1) * g16 / p.ranges);
+    }
+    if (r_hi > p.N) r_hi = p.N;
     const int k_lo = (int)((int64_t)rank * p.nkb / p.split), k_hi = (int)((int64_t)(rank + 1) * p.nkb / p.split);
-    const int nk = k_hi - k_lo;
+    const int ng = (k_hi - k_lo + GRP - 1) / GRP;                     // groups of a tile
     pdl_wait();
 
-    float acc[C::CPT];
+    if (warp < 4) {
+        const int row = warp * 32 + lane;
+        const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
+        float *svec = reinterpret_cast<float *>(sm + C::svec);
+        float *tile_o = reinterpret_cast<float *>(sm + C::tile);
+        // scales of a group, fetched a group ahead: this thread's entries (k-block j, token c)
+        constexpr int E = (GRP * NT + 127) / 128;
+        float na[E], nw[E][2];
+        auto fetch = [&](int x0, int g) {
+            const int b0 = x0 >> 7, b1 = b0 + 1 < p.tiles_x ? b0 + 1 : b0;
 #pragma unroll
-    for (int i = 0; i < C::CPT; ++i) acc[i] = 0.f;
-    bool ok = true;
-
-    if (warp < C::EW) {
-        const int half = warp >> 2;                                   // which CPT columns
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * C::CPT;
-        // scales of a group of four k-blocks, fetched one group ahead: of the
-        // thread's own row, or (SWAP) of the columns, shared by the four warps.
-        // They go through shared memory in both forms so that the loop over
-        // k-blocks is one small body: unrolled over a group it drove the
-        // producer's and the MMA warp's code out of the instruction cache, and
-        // each of their steps took ~350 cycles.
-        constexpr int NS = SWAP ? NT : C::EW * 32;
-        float *svec = reinterpret_cast<float *>(sm + C::svec);        // [2][4][NS]
-        float next[4];
-        const int sr = SWAP ? y0 + (int)threadIdx.x : x0 + row;
-        const bool mine = sr < p.M && (SWAP ? (int)threadIdx.x < NT : y0 + half * 128 < p.N);
-        const float *sa = p.a_scale + (size_t)(mine ? sr : 0) * p.nkb;
-        const float *sw = p.w_scale + (size_t)(SWAP ? tx : mine ? (y0 + half * 128) / 128 : 0) * p.nkb;
-        auto fetch = [&](int k) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) next[j] = mine && k + j < k_hi ? __ldg(sa + k + j) * __ldg(sw + k + j) : 0.f;
+            for (int e = 0; e < E; ++e) {
+                const int i = e * 128 + threadIdx.x, j = i / NT, c = i - j * NT, k = k_lo + g * GRP + j;
+                const bool in = i < GRP * NT && k < k_hi && y0 + c < p.M;
+                na[e] = in ? __ldg(p.a_scale + (size_t)(y0 + c) * p.nkb + k) : 0.f;
+                nw[e][0] = in ? __ldg(p.w_scale + (size_t)b0 * p.nkb + k) : 0.f;
+                nw[e][1] = in ? __ldg(p.w_scale + (size_t)b1 * p.nkb + k) : 0.f;
+            }
         };
-        fetch(k_lo);
+        int it = 0;
+        bool ok = true;
+        fetch(r_lo, 0);
 #pragma unroll 1
-        for (int it = 0; it < nk; ++it) {
-            if ((it & 3) == 0) {                   // (after an abort too: the warps meet at barrier 1)
-                float *sv = svec + ((it >> 2) & 1) * 4 * NS;
-                if (!SWAP || (int)threadIdx.x < NT) {
+        for (int x0 = r_lo; x0 < r_hi; x0 += 128) {
+            float acc[NT];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) sv[j * NS + threadIdx.x] = next[j];
+            for (int c = 0; c < NT; ++c) acc[c] = 0.f;
+            const int blk = ((x0 + row) >> 7) - (x0 >> 7);            // 0 or 1: the row's weight block in the tile
+#pragma unroll 1
+            for (int g = 0; g < ng; ++g, ++it) {
+                const int set = it & 1;
+                float *sv = svec + set * 2 * GRP * NT;                // [2][GRP][NT]
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i = e * 128 + threadIdx.x;
+                    if (i < GRP * NT) {
+                        sv[i] = na[e] * nw[e][0];
+                        sv[GRP * NT + i] = na[e] * nw[e][1];
+                    }
                 }
-                if (SWAP) asm volatile("bar.sync 1, 128;" ::: "memory");
-                fetch(k_lo + it + 4);
-            }
-            if (!ok) continue;
-            const float *sv = svec + (it & 7) * NS;
-            const float own_scale = SWAP ? 0.f : sv[threadIdx.x];
-            const int buf = it % C::nbuf;
-            ok = __all_sync(~0u, wait_bar_near(b_tfull + 8 * buf, (it / C::nbuf) & 1, abort_flag, p.status));
-            if (!ok) continue;
-            tc_fence_after();
-            constexpr int W = C::CPT < 32 ? 16 : 32;
+                asm volatile("bar.sync 1, 128;" ::: "memory");        // (after an abort too: all four warps come here)
+                if (g + 1 < ng) fetch(x0, g + 1);
+                else if (x0 + 128 < r_hi) fetch(x0 + 128, 0);
+                if (ok) ok = __all_sync(~0u, wait_bar_near(b_tfull + 8 * set, (it >> 1) & 1, abort_flag, p.status));
+                if (!ok) continue;
+                tc_fence_after();
+                const float *s = sv + blk * GRP * NT;
+                const int here = k_hi - k_lo - g * GRP;               // blocks of this group
+                // chunks of 16 columns, the next on its way while one is added
+                constexpr int CH = GRP * NT / 16;
+                uint32_t v[2][16];
+                tmem_ld16(t_row + set * GRP * NT, v[0]);
 #pragma unroll
-            for (int c = 0; c < C::CPT; c += W) {
-                uint32_t v[W];
-                if constexpr (W == 32) tmem_ld32(t_row + buf * NT + c, v);
-                else tmem_ld16(t_row + buf * NT + c, v);
-                tmem_wait_ld();
+                for (int c = 0; c < CH; ++c) {
+                    tmem_wait_ld();
+                    if (c + 1 < CH) {
+                        tmem_ld16(t_row + set * GRP * NT + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_tempty + 8 * set);
+                    }
+                    const uint32_t(&w)[16] = v[c & 1];
+                    constexpr int per = NT / 16;
+                    const int j = c / per, c0 = c % per * 16;
+                    if (j < here) {                                   // (buffers past the last block hold old sums)
 #pragma unroll
-                for (int q = 0; q < W; q += 4) {
-                    const float4 s = SWAP ? *reinterpret_cast<const float4 *>(sv + c + q)
-                                          : make_float4(own_scale, own_scale, own_scale, own_scale);
-                    const float2 u = ffma2(make_float2(__uint_as_float(v[q]), __uint_as_float(v[q + 1])),
-                                           make_float2(s.x, s.y), make_float2(acc[c + q], acc[c + q + 1]));
-                    const float2 w = ffma2(make_float2(__uint_as_float(v[q + 2]), __uint_as_float(v[q + 3])),
-                                           make_float2(s.z, s.w), make_float2(acc[c + q + 2], acc[c + q + 3]));
-                    acc[c + q] = u.x, acc[c + q + 1] = u.y, acc[c + q + 2] = w.x, acc[c + q + 3] = w.y;
+                        for (int q = 0; q < 16; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(s + j * NT + c0 + q);
+                            acc[c0 + q] = fmaf(__uint_as_float(w[q]), f.x, acc[c0 + q]);
+                            acc[c0 + q + 1] = fmaf(__uint_as_float(w[q + 1]), f.y, acc[c0 + q + 1]);
+                            acc[c0 + q + 2] = fmaf(__uint_as_float(w[q + 2]), f.z, acc[c0 + q + 2]);
+                            acc[c0 + q + 3] = fmaf(__uint_as_float(w[q + 3]), f.w, acc[c0 + q + 3]);
+                        }
+                    }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b_tempty + 8 * buf);
+            // ---- out: through shared memory, so that the stores are runs of a token's row
+#pragma unroll
+            for (int c = 0; c < NT; ++c) tile_o[c * 128 + row] = acc[c];
+            if (p.split > 1) break;                                   // (one tile: joined below)
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int rows = r_hi - x0 < 128 ? r_hi - x0 : 128;
+            if (!*abort_flag) {
+#pragma unroll 1
+                for (int c = warp; c < NT && y0 + c < p.M; c += 4)
+                    if (lane * 4 < rows)
+                        put4_any(p, (size_t)(y0 + c) * p.N + x0 + lane * 4,
+                                 *reinterpret_cast<const float4 *>(tile_o + c * 128 + lane * 4), rows - lane * 4);
+            }
+            // (the next tile's sums are written after the group barriers above: at least one)
         }
-    } else if (warp == C::EW) {
-        if (lane == 0) {
-            const uint64_t first = make_policy_evict_first(), last = make_policy_evict_last();
-            const uint64_t px = SWAP ? first : last;                  // streamed once, or re-read by other tiles
-            const int ns = (nk + CPS - 1) / CPS;
+    } else if (warp == 4) {
+        if (elect_one()) {
+            const uint64_t once = make_policy_evict_first(), keep = make_policy_evict_last();
+            const uint64_t pw = p.tiles_y > 1 ? keep : once;
             int it = 0;
-            for (; it < ns; ++it) {
-                const int st = it % C::nst, n = it / C::nst;
-                if (n > 0 && !wait_bar_near(b_empty + 8 * st, (n - 1) & 1, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
-                const int here = nk - it * CPS < CPS ? nk - it * CPS : CPS;
-                const uint32_t full = b_full + 8 * st, dx = base + st * C::stage, dy = dx + CPS * kXBytes;
-                mbar_expect_tx(full, here * (kXBytes + NT * 128));
-                for (int j = 0; j < here; ++j) {
-                    const int k = (k_lo + it * CPS + j) * 128;
-                    tma_load_2d_hint(dx + j * kXBytes, &mp.x, full, k, x0, px);
-                    tma_load_2d_hint(dy + j * NT * 128, &mp.y, full, k, y0, last);
+            bool ok = true;
+            for (int x0 = r_lo; x0 < r_hi && ok; x0 += 128) {
+                const int rows = r_hi - x0 < 128 ? (r_hi - x0 + 15) & ~15 : 128;
+#pragma unroll 1
+                for (int g = 0; g < ng; ++g, ++it) {
+                    const int st = it % NST, n = it / NST;
+                    if (n > 0) ok = wait_bar_near(b_empty + 8 * st, (n - 1) & 1, abort_flag, p.status);
+                    if (!ok) break;
+                    const int k0 = k_lo + g * GRP, here = k_hi - k0 < GRP ? k_hi - k0 : GRP;
+                    const uint32_t full = b_full + 8 * st, dx = base + st * C::stage, dy = dx + GRP * kXBytes;
+                    mbar_expect_tx(full, here * (rows * 128 + NT * 128));
+                    for (int j = 0; j < here; ++j) {
+                        if (rows == 128) {
+                            tma_load_2d_hint(dx + j * kXBytes, &mp.w, full, (k0 + j) * 128, x0, pw);
+                        } else {
+                            for (int r = 0; r < rows; r += 16)
+                                tma_load_2d_hint(dx + j * kXBytes + r * 128, &mp.w16, full, (k0 + j) * 128, x0 + r, pw);
+                        }
+                    }
+                    for (int j = 0; j < here; ++j)
+                        tma_load_2d_hint(dy + j * NT * 128, &mp.a, full, (k0 + j) * 128, y0, keep);
                 }
             }
             if (!ok) {                                                // abort: let the copies in flight land
-                for (int st = 0; st < C::nst; ++st) {
-                    const int fills = it / C::nst + (st < it % C::nst ? 1 : 0);
+                for (int st = 0; st < NST; ++st) {
+                    const int fills = it / NST + (st < it % NST ? 1 : 0);
                     if (fills) wait_bar_quiet(b_full + 8 * st, (fills - 1) & 1);
                 }
             }
         }
         __syncwarp();
     } else {
-        if (lane == 0) {
-            const uint32_t idesc = instr_desc_e4m3(128, NT);
-            const int ns = (nk + CPS - 1) / CPS;
-            for (int it = 0; it < ns && ok; ++it) {
-                const int st = it % C::nst;
-                if (!wait_bar_near(b_full + 8 * st, (it / C::nst) & 1, abort_flag, p.status)) {
-                    ok = false;
-                    break;
-                }
+        if (elect_one()) {
+            constexpr uint32_t idesc = instr_desc_e4m3(128, NT);
+            const int steps = (r_hi - r_lo + 127) / 128 * ng;
+            bool ok = true;
+            int g = 0;
+#pragma unroll 1
+            for (int it = 0; it < steps; ++it) {
+                const int st = it % NST, set = it & 1, n = it >> 1;
+                ok = wait_bar_near(b_full + 8 * st, (it / NST) & 1, abort_flag, p.status) &&
+                     (n == 0 || wait_bar_near(b_tempty + 8 * set, (n - 1) & 1, abort_flag, p.status));
+                if (!ok) break;
                 tc_fence_after();
-                for (int j = 0; j < CPS && it * CPS + j < nk; ++j) {
-                    const int kb = it * CPS + j, buf = kb % C::nbuf, n = kb / C::nbuf;
-                    if (n > 0 && !wait_bar_near(b_tempty + 8 * buf, (n - 1) & 1, abort_flag, p.status)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t dx = base + st * C::stage + j * kXBytes,
-                                   dy = base + st * C::stage + CPS * kXBytes + j * NT * 128;
-                    const uint64_t ax = smem_desc(dx, 16, 1024), ay = smem_desc(dy, 16, 1024);
+                const int here = k_hi - k_lo - g * GRP;
+                if (++g == ng) g = 0;
+                const uint32_t dx = base + st * C::stage;
+                const uint64_t aw = smem_desc(dx, 16, 1024), at = smem_desc(dx + GRP * kXBytes, 16, 1024);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tc_mma_f8(tmem + buf * NT, ax + 2 * q, ay + 2 * q, idesc, q);
-                    tc_commit(b_tfull + 8 * buf);
+                for (int j = 0; j < GRP; ++j) {
+                    if (j < here) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc_mma_f8(tmem + (set * GRP + j) * NT, aw + j * (kXBytes >> 4) + 2 * q,
+                                      at + j * (NT * 128 >> 4) + 2 * q, idesc, q);
+                    }
                 }
-                if (ok) tc_commit(b_empty + 8 * st);
+                tc_commit(b_tfull + 8 * set);
+                tc_commit(b_empty + 8 * st);
             }
             if (!ok) {
                 tc_commit(b_drain);
@@ -262,54 +319,31 @@ __global__ void __launch_bounds__(Conf<NT, SWAP, CPS>::threads, 1)
         __syncwarp();
     }
 
-    // ---- output: the tile goes through shared memory (the ring: every load has
-    // been consumed) so that the stores are whole rows of it; with a split each
-    // rank writes its share of the token rows, added over the ranks in order.
-    float *tile_o = reinterpret_cast<float *>(sm);
-    __syncthreads();
-    if (warp < C::EW) {
-        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-        if (SWAP) {
-#pragma unroll
-            for (int c = 0; c < C::CPT; ++c) tile_o[c * C::pitch + row] = acc[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < C::CPT; c += 4)
-                *reinterpret_cast<float4 *>(tile_o + row * C::pitch + half * C::CPT + c) =
-                    make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-        }
-    }
-    if (p.split > 1) cluster_sync();
-    else __syncthreads();
-    const int m0 = SWAP ? y0 : x0, n0 = SWAP ? x0 : y0;
-    if (!*abort_flag) {
-        constexpr int per = C::len / 4;                               // threads of a token row
+    if (p.split > 1) {
+        // each rank writes its share of the token rows, added over the ranks in order
+        cluster_sync();
+        if (!*abort_flag) {
 #pragma unroll 1
-        for (int i = threadIdx.x; i < C::lines * per; i += C::threads) {
-            const int line = i / per, e = (i % per) * 4;
-            const int m = m0 + line, n = n0 + e;
-            if (m >= p.M || n >= p.N || (p.split > 1 && line % p.split != rank)) continue;
-            float4 x;
-            if (p.split > 1) {
-                x = make_float4(0.f, 0.f, 0.f, 0.f);
-                const uint32_t at = base + (uint32_t)(line * C::pitch + e) * 4u;
-                for (int r = 0; r < p.split; ++r) {
-                    const float4 v = ld_cluster_f32x4(at, r);
-                    x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
-                }
-            } else {
-                x = *reinterpret_cast<const float4 *>(tile_o + line * C::pitch + e);
+            for (int c = rank + warp * p.split; c < NT; c += 6 * p.split) {
+                const int n = r_lo + lane * 4;
+                if (y0 + c >= p.M || n >= p.N) continue;
+                const uint32_t at = base + C::tile + (uint32_t)(c * 128 + lane * 4) * 4u;
+                float4 v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < p.split) v[r] = ld_cluster_f32x4(at, r);
+                float4 x = v[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < p.split) x.x += v[r].x, x.y += v[r].y, x.z += v[r].z, x.w += v[r].w;
+                put4_any(p, (size_t)(y0 + c) * p.N + n, x, p.N - n);
             }
-            const size_t at = (size_t)m * p.N + n;
-            if (p.out_dtype == ORTHRUS_BF16) put4(static_cast<__nv_bfloat16 *>(p.out) + at, x, p.N - n, p.vec);
-            else if (p.out_dtype == ORTHRUS_F16) put4(static_cast<__half *>(p.out) + at, x, p.N - n, p.vec);
-            else put4(static_cast<float *>(p.out) + at, x, p.N - n, p.vec);
         }
+        cluster_sync_relaxed();                                       // no block leaves while its partials are read
     }
-    if (p.split > 1) cluster_sync();                                  // no block leaves while its partials are read
     tc_fence_before();
     __syncthreads();
-    if (warp == C::EW + 1) {
+    if (warp == 5) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::cols) : "memory");
     }
@@ -325,43 +359,47 @@ namespace f8 {
 
 constexpr int kMaxDevices = 64;
 
-template <int NT, bool SWAP, int CPS> bool smem_ready(int dev)
+template <int NT, int GRP, int NST> bool rows_ready(int dev)
 {
     static std::once_flag once[kMaxDevices];
     static bool ok[kMaxDevices];
     if (dev < 0 || dev >= kMaxDevices) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(fp8_matmul_kernel<NT, SWAP, CPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Conf<NT, SWAP, CPS>::total) == cudaSuccess;
+        ok[dev] = cudaFuncSetAttribute(fp8_rows_kernel<NT, GRP, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Conf<NT, GRP, NST>::total) == cudaSuccess;
         if (!ok[dev]) cudaGetLastError();
     });
     return ok[dev];
 }
 
-template <int NT, bool SWAP, int CPS>
-int launch(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t st)
+template <int NT, int GRP, int NST>
+int launch_rows(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t st)
 {
-    using C = Conf<NT, SWAP, CPS>;
-    static_assert(C::total <= 227 * 1024, "shared memory");
-    const void *x = SWAP ? w : a, *y = SWAP ? a : w;
-    const int xr = SWAP ? p.N : p.M, yr = SWAP ? p.M : p.N;
-    p.tiles_x = (xr + 127) / 128;
-    p.tiles_y = (yr + NT - 1) / NT;
+    using C = Conf<NT, GRP, NST>;
+    p.tiles_x = (p.N + 127) / 128;
+    p.tiles_y = (p.M + NT - 1) / NT;
+    p.vec = ((uintptr_t)p.out & (uintptr_t)(4 * elem_size(p.out_dtype) - 1)) == 0 && p.N % 4 == 0;
     const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
-    // fewer tiles than half the SMs: split K over a cluster
+    // fewer tiles than half the SMs: split K over a cluster; else 16-row granules over the SMs
     int split = (int)(tiles * 2 <= sms ? sms / tiles : 1);
     if (split > 8) split = 8;
     if (split > p.nkb) split = p.nkb;
     p.split = split;
-    if (tiles * split >= 1ll << 31) return ORTHRUS_ERR_UNSUPPORTED;
+    const int g16 = (p.N + 15) / 16;
+    p.ranges = p.tiles_y >= sms ? 1 : sms / p.tiles_y;
+    if (p.ranges > g16) p.ranges = g16;
+    const int64_t blocks = split > 1 ? tiles * split : (int64_t)p.ranges * p.tiles_y;
+    if (blocks >= 1ll << 31) return ORTHRUS_ERR_UNSUPPORTED;
     Maps mp;
     const uint64_t str[1] = {(uint64_t)p.K};
-    const uint64_t dx[2] = {(uint64_t)p.K, (uint64_t)xr}, dy[2] = {(uint64_t)p.K, (uint64_t)yr};
-    const uint32_t bx[2] = {128, 128}, by[2] = {128, NT};
-    if (!encode_u8_sw128(&mp.x, 2, x, dx, str, bx) || !encode_u8_sw128(&mp.y, 2, y, dy, str, by)) return ORTHRUS_ERR_LAUNCH;
-    if (!smem_ready<NT, SWAP, CPS>(dev)) return ORTHRUS_ERR_LAUNCH;
+    const uint64_t dw[2] = {(uint64_t)p.K, (uint64_t)p.N}, da[2] = {(uint64_t)p.K, (uint64_t)p.M};
+    const uint32_t bw[2] = {128, 128}, b16[2] = {128, 16}, ba[2] = {128, NT};
+    if (!encode_u8_sw128(&mp.w, 2, w, dw, str, bw) || !encode_u8_sw128(&mp.w16, 2, w, dw, str, b16) ||
+        !encode_u8_sw128(&mp.a, 2, a, da, str, ba))
+        return ORTHRUS_ERR_LAUNCH;
+    if (!rows_ready<NT, GRP, NST>(dev)) return ORTHRUS_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(C::threads);
     cfg.dynamicSmemBytes = C::total;
     cfg.stream = st;
@@ -374,7 +412,7 @@ int launch(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_matmul_kernel<NT, SWAP, CPS>, mp, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_rows_kernel<NT, GRP, NST>, mp, p);
     return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
 }
 
@@ -469,11 +507,10 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     p.K = K;
     p.nkb = (K + ORTHRUS_FP8_BLOCK - 1) / ORTHRUS_FP8_BLOCK;
     p.out_dtype = out_dtype;
-    p.vec = ((uintptr_t)out & (uintptr_t)(4 * e - 1)) == 0 && N % 4 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M <= 16) return f8::launch<16, true, 4>(p, a, w, dev, sms, st);
-    if (M <= 32) return f8::launch<32, true, 4>(p, a, w, dev, sms, st);
-    if (M <= 64) return f8::launch<64, true, 2>(p, a, w, dev, sms, st);
-    if (M <= 128) return f8::launch<128, true, 2>(p, a, w, dev, sms, st);
+    if (M <= 16) return f8::launch_rows<16, 4, 3>(p, a, w, dev, sms, st);
+    if (M <= 32) return f8::launch_rows<32, 4, 2>(p, a, w, dev, sms, st);
+    if (M <= 64) return f8::launch_rows<64, 2, 3>(p, a, w, dev, sms, st);
+    if (M <= 128 || ORTHRUS_FORCE_ROWS) return f8::launch_rows<128, 2, 2>(p, a, w, dev, sms, st);
     return f8::launch_pair(p, a, w, dev, sms, st);
 }
