@@ -8,6 +8,7 @@ library is missing or the device cannot run it, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -330,7 +331,11 @@ def orthrus_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 
 
 # ---------------------------------------------------------------- layer operators
+# (These calls are short on the GPU, so their argument checks are kept to what a
+# few attribute reads per tensor cost.)
 _CODES = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _code(dt: torch.dtype) -> int:
@@ -340,41 +345,39 @@ def _code(dt: torch.dtype) -> int:
     return code
 
 
-def _same(tensors, dtype: torch.dtype) -> None:
-    for t in tensors:
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"expected {dtype}, got {t.dtype}")
+def _fail(t: torch.Tensor, dtype, shape, dev):
+    if t.get_device() < 0:
+        raise ValueError("liborthrus takes device tensors")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"tensors on devices {dev} and {t.get_device()}")
+    raise ValueError("liborthrus takes contiguous tensors here")
 
 
-def _shape(t: torch.Tensor, *shape) -> None:
-    if t.shape != shape:
-        raise ValueError(f"expected shape {shape}, got {tuple(t.shape)}")
+def _dense(t: Optional[torch.Tensor], dtype, shape, dev: int):
+    """Address of a contiguous tensor of this type and shape on device `dev`
+    (None stays None; a None type or shape is not checked)."""
+    if t is None:
+        return None
+    if ((dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape)
+            or t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+        _fail(t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _where(tensors, stream):
-    """The device index all tensors share and the raw stream the call goes to
-    (by default that device's current one)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("liborthrus takes device tensors")
-        d = t.get_device()
-        if dev is None:
-            dev = d
-        elif d != dev:
-            raise ValueError(f"tensors on devices {dev} and {d}")
-    if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
-    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _strided(t: torch.Tensor, dtype, shape, dev: int):
+    """The same for a tensor whose strides are passed along."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
+        _fail(t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _launch(name: str, dev: int, *args) -> None:
+def _launch(name: str, fn, dev: int, *args) -> None:
     """Call the entry point with the tensors' device current."""
-    fn = getattr(lib(), name)
-    now = torch._C._cuda_getDevice()
-    if now == dev:
+    if _current_device() == dev:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -383,14 +386,11 @@ def _launch(name: str, dev: int, *args) -> None:
         _check(name, rc)
 
 
-def _dense(*tensors) -> None:
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("liborthrus takes contiguous tensors here")
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _on(stream, dev: int) -> int:
+    """The raw stream a call goes to: by default the tensors' device's current one."""
+    if stream is None:
+        return _raw_stream(dev) if dev >= 0 else 0
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(x: torch.Tensor):
@@ -411,34 +411,24 @@ def orthrus_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Opti
     and / or out_fp8 [T,H] e4m3 with out_scale [T,ceil(H/128)] fp32; with a
     residual [T,H], x + residual is normed and written to sum_out."""
     T, H, stride = _rows(x)
-    _same((weight, out, residual, sum_out), x.dtype)
-    _shape(weight, H)
-    for t in (out, residual, sum_out, out_fp8):
-        if t is not None:
-            _shape(t, T, H)
-    if out_fp8 is not None:
-        _same((out_fp8,), torch.float8_e4m3fn)
-    if out_scale is not None:
-        _same((out_scale,), torch.float32)
-        _shape(out_scale, T, (H + 127) // 128)
-    _dense(weight, out, residual, sum_out, out_fp8, out_scale)
-    dev, st = _where((x, weight, out, residual, sum_out, out_fp8, out_scale), stream)
-    _launch("orthrus_rmsnorm", dev, _code(x.dtype), x.data_ptr(), stride, _addr(residual), weight.data_ptr(), T, H,
-            eps, _addr(sum_out), _addr(out), _addr(out_fp8), _addr(out_scale), st)
+    dt, dev, shape = x.dtype, x.get_device(), x.shape
+    pw = _dense(weight, dt, (H,), dev)
+    po, pr, ps = _dense(out, dt, shape, dev), _dense(residual, dt, shape, dev), _dense(sum_out, dt, shape, dev)
+    pq = _dense(out_fp8, torch.float8_e4m3fn, shape, dev)
+    pc = _dense(out_scale, torch.float32, (T, (H + 127) // 128), dev)
+    _launch("orthrus_rmsnorm", lib().orthrus_rmsnorm, dev, _code(dt), x.data_ptr(), stride, pr, pw, T, H, eps, ps, po,
+            pq, pc, _on(stream, dev))
 
 
 def orthrus_quantize_fp8(x: torch.Tensor, out_fp8: torch.Tensor, out_scale: torch.Tensor, stream=None) -> None:
     """x [T,H] (rows may be strided) -> out_fp8 [T,H] e4m3 and out_scale
     [T,ceil(H/128)] fp32, one scale per row and 128 columns."""
     T, H, stride = _rows(x)
-    _shape(out_fp8, T, H)
-    _shape(out_scale, T, (H + 127) // 128)
-    _same((out_fp8,), torch.float8_e4m3fn)
-    _same((out_scale,), torch.float32)
-    _dense(out_fp8, out_scale)
-    dev, st = _where((x, out_fp8, out_scale), stream)
-    _launch("orthrus_quantize_fp8", dev, _code(x.dtype), x.data_ptr(), stride, T, H, out_fp8.data_ptr(),
-            out_scale.data_ptr(), st)
+    dev = x.get_device()
+    pq = _dense(out_fp8, torch.float8_e4m3fn, x.shape, dev)
+    pc = _dense(out_scale, torch.float32, (T, (H + 127) // 128), dev)
+    _launch("orthrus_quantize_fp8", lib().orthrus_quantize_fp8, dev, _code(x.dtype), x.data_ptr(), stride, T, H, pq, pc,
+            _on(stream, dev))
 
 
 def orthrus_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -448,16 +438,12 @@ def orthrus_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
     M, K = a.shape
     N = w.shape[0]
     nk = (K + 127) // 128
-    _same((a, w), torch.float8_e4m3fn)
-    _same((a_scale, w_scale), torch.float32)
-    _shape(w, N, K)
-    _shape(a_scale, M, nk)
-    _shape(w_scale, (N + 127) // 128, nk)
-    _shape(out, M, N)
-    _dense(a, a_scale, w, w_scale, out, status)
-    dev, st = _where((a, a_scale, w, w_scale, out, status), stream)
-    _launch("orthrus_fp8_matmul", dev, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
-            _code(out.dtype), out.data_ptr(), _addr(status), st)
+    dev, e4m3, f32 = a.get_device(), torch.float8_e4m3fn, torch.float32
+    pa, pw = _dense(a, e4m3, None, dev), _dense(w, e4m3, (N, K), dev)
+    psa, psw = _dense(a_scale, f32, (M, nk), dev), _dense(w_scale, f32, ((N + 127) // 128, nk), dev)
+    po, pst = _dense(out, None, (M, N), dev), _dense(status, torch.int32, None, dev)
+    _launch("orthrus_fp8_matmul", lib().orthrus_fp8_matmul, dev, pa, psa, pw, psw, M, N, K, _code(out.dtype), po, pst,
+            _on(stream, dev))
 
 
 def orthrus_rope_table(rot_dim: int, theta: float, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -472,31 +458,25 @@ def orthrus_rope_table(rot_dim: int, theta: float, kind: int = ROPE_PLAIN, facto
     return turns, mag.value
 
 
-_Strides = ctypes.c_int64 * 8
+@functools.lru_cache(maxsize=256)
+def _stride_array(*strides):
+    """HOST array of eight strides (read during the call only)."""
+    return (ctypes.c_int64 * 8)(*strides)
 
 
-def _token_strides(t: torch.Tensor, lead):
-    """(token stride, head stride) of [*lead, H, D]: tokens evenly spaced, heads' elements contiguous."""
-    H, D = t.shape[-2:]
-    s = t.stride()
-    if D > 1 and s[-1] != 1:
+def _token_strides(t: torch.Tensor):
+    """(token stride, head stride) of [T, H, D] or [B, K, H, D]: tokens evenly
+    spaced, a head's elements contiguous."""
+    s, n = t.stride(), t.shape
+    if s[-1] != 1 and n[-1] > 1:
         raise ValueError("a head's elements have to be contiguous")
-    if len(lead) == 1:
+    if len(s) == 3:
         return s[0], s[1]
-    if lead[0] > 1 and lead[1] > 1 and s[0] != lead[1] * s[1]:
+    if n[1] == 1:
+        return s[0], s[2]
+    if n[0] > 1 and s[0] != n[1] * s[1]:
         raise ValueError("tokens have to be evenly spaced over sequences and block slots")
-    return (s[1] if lead[1] > 1 else s[0]), s[2]
-
-
-def _rope_common(q, k, q_out, turns, q_norm, k_norm, D, dtype):
-    rot = 2 * turns.shape[0]
-    _same((q, k, q_out, q_norm, k_norm), dtype)
-    _same((turns,), torch.float64)
-    for t in (q_norm, k_norm):
-        if t is not None:
-            _shape(t, D)
-    _dense(turns, q_norm, k_norm)
-    return rot
+    return s[1], s[2]
 
 
 def orthrus_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, turns: torch.Tensor,
@@ -507,27 +487,21 @@ def orthrus_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     positions [T] int32 -> q_out, k_out (may be q and k themselves).  turns
     [rot/2] float64 on the device and magnitude: from orthrus_rope_table."""
     T, Hq, D = q.shape
-    rot = _rope_common(q, k, q_out, turns, q_norm, k_norm, D, q.dtype)
-    _same((positions,), torch.int32)
-    _shape(positions, T)
-    _shape(q_out, T, Hq, D)
-    lead, Hkv = (T,), 0
-    st4 = _token_strides(q, lead) + _token_strides(q_out, lead)
+    dt, dev = q.dtype, q.get_device()
+    pq, pqo = _strided(q, dt, q.shape, dev), _strided(q_out, dt, q.shape, dev)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     if k is not None:
         Hkv = k.shape[1]
-        _shape(k, T, Hkv, D)
-        _shape(k_out, T, Hkv, D)
-        _same((k_out,), q.dtype)
-        st4 += _token_strides(k, lead) + _token_strides(k_out, lead)
+        pk, pko = _strided(k, dt, (T, Hkv, D), dev), _strided(k_out, dt, (T, Hkv, D), dev)
+        st = _stride_array(*_token_strides(q), *_token_strides(q_out), *_token_strides(k), *_token_strides(k_out))
     else:
-        st4 += (0, 0, 0, 0)
-    _dense(positions)
-    dev, st = _where((q, k, positions, turns, q_out, k_out, q_norm, k_norm), stream)
-    _launch("orthrus_rope", dev, _code(q.dtype), layout, q.data_ptr(), q_out.data_ptr(), _addr(k), _addr(k_out),
-            _Strides(*st4), positions.data_ptr(), turns.data_ptr(), magnitude, T, Hq, Hkv, D, rot, _addr(q_norm),
-            _addr(k_norm), eps, st)
+        Hkv, pk, pko = 0, None, None
+        st = _stride_array(*_token_strides(q), *_token_strides(q_out), 0, 0, 0, 0)
+    pp, pt = _dense(positions, torch.int32, (T,), dev), _dense(turns, torch.float64, None, dev)
+    pqn, pkn = _dense(q_norm, dt, (D,), dev), _dense(k_norm, dt, (D,), dev)
+    _launch("orthrus_rope", lib().orthrus_rope, dev, _code(dt), layout, pq, pqo, pk, pko, st, pp, pt, magnitude, T, Hq,
+            Hkv, D, 2 * turns.shape[0], pqn, pkn, eps, _on(stream, dev))
 
 
 def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -543,42 +517,34 @@ def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v:
     None too)."""
     P, Hkv, page, D = k_pages.shape
     B, max_pages = block_table.shape
-    dtype = k_pages.dtype
-    rot = _rope_common(q, k, q_out, turns, q_norm, k_norm, D, dtype)
-    _same((v, v_pages), dtype)
-    _same((block_table, ctx_lens), torch.int32)
-    _shape(ctx_lens, B)
+    dt, dev = k_pages.dtype, k_pages.get_device()
     if (q is None) != (q_out is None) or (k is None) != (v is None):
         raise ValueError("q and q_out, and k and v, go together")
-    n = q if q is not None else k
-    if n is not None:
-        K = n.shape[1]
+    if q is not None:
+        K, Hq = q.shape[1], q.shape[2]
+        pq, pqo = _strided(q, dt, (B, K, Hq, D), dev), _strided(q_out, dt, (B, K, Hq, D), dev)
+        st = _token_strides(q) + _token_strides(q_out)
+    else:
+        Hq, pq, pqo, st = 0, None, None, (0, 0, 0, 0)
+        if k is not None:
+            K = k.shape[1]
     if K is None:
         raise ValueError("the number of tokens per sequence is not known: give K")
-    lead, Hq, st8 = (B, K), 0, ()
-    if q is not None:
-        Hq = q.shape[2]
-        _shape(q, B, K, Hq, D)
-        _shape(q_out, B, K, Hq, D)
-        st8 += _token_strides(q, lead) + _token_strides(q_out, lead)
-    else:
-        st8 += (0, 0, 0, 0)
     if k is not None:
         if v_pages is None:
             raise ValueError("v needs v_pages")
-        _shape(k, B, K, Hkv, D)
-        _shape(v, B, K, Hkv, D)
-        st8 += _token_strides(k, lead) + _token_strides(v, lead)
+        pk, pv = _strided(k, dt, (B, K, Hkv, D), dev), _strided(v, dt, (B, K, Hkv, D), dev)
+        st = _stride_array(*st, *_token_strides(k), *_token_strides(v))
     else:
-        st8 += (0, 0, 0, 0)
-    if v_pages is not None:
-        _shape(v_pages, P, Hkv, page, D)
-    _dense(k_pages, v_pages, block_table, ctx_lens, status)
-    dev, st = _where((q, k, v, turns, q_out, k_pages, v_pages, block_table, ctx_lens, q_norm, k_norm, status), stream)
-    _launch("orthrus_rope_append", dev, _code(dtype), layout, _addr(q), _addr(q_out), _addr(k), _addr(v),
-            _Strides(*st8), turns.data_ptr(), magnitude, B, K, Hq, Hkv, D, rot, _addr(q_norm), _addr(k_norm), eps,
-            k_pages.data_ptr(), _addr(v_pages), P, page, block_table.data_ptr(), max_pages, ctx_lens.data_ptr(),
-            _addr(status), st)
+        pk, pv = None, None
+        st = _stride_array(*st, 0, 0, 0, 0)
+    pt, pkp, pvp = _dense(turns, torch.float64, None, dev), _dense(k_pages, dt, None, dev), _dense(
+        v_pages, dt, k_pages.shape, dev)
+    pb, pc = _dense(block_table, torch.int32, None, dev), _dense(ctx_lens, torch.int32, (B,), dev)
+    pqn, pkn = _dense(q_norm, dt, (D,), dev), _dense(k_norm, dt, (D,), dev)
+    _launch("orthrus_rope_append", lib().orthrus_rope_append, dev, _code(dt), layout, pq, pqo, pk, pv, st, pt, magnitude,
+            B, K, Hq, Hkv, D, 2 * turns.shape[0], pqn, pkn, eps, pkp, pvp, P, page, pb, max_pages, pc,
+            _dense(status, torch.int32, None, dev), _on(stream, dev))
 
 
 def orthrus_paged_attn_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -592,17 +558,14 @@ def orthrus_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     [B,max_pages] int32, ctx_lens [B] int32 -> out [B,Hq,D]: attention of one
     token per sequence over keys [0, ctx_lens[b] + n_new)."""
     B, Hq, D = q.shape
-    P, Hkv, page, _ = k_pages.shape
-    _same((k_pages, v_pages, out), q.dtype)
-    _same((block_table, ctx_lens), torch.int32)
-    _shape(k_pages, P, Hkv, page, D)
-    _shape(v_pages, P, Hkv, page, D)
-    _shape(out, B, Hq, D)
-    _shape(ctx_lens, B)
+    P, Hkv, page, Dk = k_pages.shape
     max_pages = block_table.shape[1]
-    _shape(block_table, B, max_pages)
-    _dense(q, k_pages, v_pages, block_table, ctx_lens, out, workspace, status)
-    dev, st = _where((q, k_pages, v_pages, block_table, ctx_lens, out, workspace, status), stream)
-    _launch("orthrus_paged_attn", dev, _code(q.dtype), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            block_table.data_ptr(), ctx_lens.data_ptr(), n_new, B, Hq, Hkv, D, P, page, max_pages, scale,
-            out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(status), st)
+    if Dk != D:
+        raise ValueError(f"head size {D} of q and {Dk} of the pages")
+    dt, dev = q.dtype, q.get_device()
+    pq, po = _dense(q, dt, None, dev), _dense(out, dt, q.shape, dev)
+    pk, pv = _dense(k_pages, dt, None, dev), _dense(v_pages, dt, k_pages.shape, dev)
+    pb, pc = _dense(block_table, torch.int32, (B, max_pages), dev), _dense(ctx_lens, torch.int32, (B,), dev)
+    pw, pst = _dense(workspace, None, None, dev), _dense(status, torch.int32, None, dev)
+    _launch("orthrus_paged_attn", lib().orthrus_paged_attn, dev, _code(dt), pq, pk, pv, pb, pc, n_new, B, Hq, Hkv, D, P,
+            page, max_pages, scale, po, pw, workspace.nbytes, pst, _on(stream, dev))

@@ -28,10 +28,6 @@
 #include "kernels.h"
 #include "layer_ops.cuh"
 
-#ifndef ORTHRUS_FORCE_ROWS
-#define ORTHRUS_FORCE_ROWS 0
-#endif
-
 namespace orthrus {
 
 namespace f8 {
@@ -511,6 +507,10 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     if (M <= 16) return f8::launch_rows<16, 4, 3>(p, a, w, dev, sms, st);
     if (M <= 32) return f8::launch_rows<32, 4, 2>(p, a, w, dev, sms, st);
     if (M <= 64) return f8::launch_rows<64, 2, 3>(p, a, w, dev, sms, st);
-    if (M <= 128 || ORTHRUS_FORCE_ROWS) return f8::launch_rows<128, 2, 2>(p, a, w, dev, sms, st);
+    // Pairs from 129 rows on, unless their 256 x 256 tiles (no K split) leave most
+    // SMs idle: 256 x 4096 x 12288 (16 tiles) takes 30 us by rows and 54 by pairs,
+    // 256 x 6144 x 4096 (24) 22 and 22, 512 x 6144 x 4096 (48) 40 and 23.
+    const int64_t pair_tiles = (int64_t)((M + 255) / 256) * ((N + f8::kPairN - 1) / f8::kPairN);
+    if (M <= 128 || pair_tiles * 6 <= sms) return f8::launch_rows<128, 2, 2>(p, a, w, dev, sms, st);
     return f8::launch_pair(p, a, w, dev, sms, st);
 }
