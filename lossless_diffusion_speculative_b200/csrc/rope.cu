@@ -8,13 +8,14 @@
 // angle would be off by 2^-4 radians.  sincospi then gets an fp32 fraction in
 // [-1, 1], good to 2^-24 of a half turn.
 //
-// Vector path: a block takes `tile` tokens; its threads first compute the
-// tile's (cos, sin) pairs into shared memory, once for all heads, then walk
-// (token, head) items with LP lanes of 16 values each.  A lane's two 8-value
-// vectors are the two sides of 8 pairs (halves layout: elements 8u.. and
-// rot/2 + 8u..; interleaved: 16u..16u+15), so a rotation needs no exchange
-// between lanes; the norm's sum of squares is a shuffle over the LP lanes.
-// HBM-bound: every value is read and written once.
+// Vector path: a warp takes a token and a run of its heads, LP lanes of 16
+// values each per head.  A lane's two 8-value vectors are the two sides of 8
+// pairs (halves layout: elements 8u.. and rot/2 + 8u..; interleaved:
+// 16u..16u+15), so a rotation needs no exchange between lanes and the lane's 8
+// (cos, sin) pairs stay in registers for all of its heads (each computed by one
+// lane, passed on through shared memory); the norm's sum of squares is a shuffle
+// over the LP lanes.  U heads' loads are issued before any of them is worked on
+// and before the angles are.  HBM-bound: every value is read and written once.
 //
 // Element path (misaligned tensors, D or rot not a multiple of 16): a warp per
 // (token, head), lanes over single pairs.
@@ -117,84 +118,102 @@ __device__ __forceinline__ float2 cos_sin(const RopeArgs &p, int pos, int i)
 }
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTile = 8;
 
-template <typename T, int LP>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p, int tile)
+template <typename T, int LP, int U>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p, int run, int runs, int64_t units)
 {
-    extern __shared__ float2 cs[];                    // [tile][rot / 2]
-    __shared__ int64_t crow[kRopeMaxTile];
+    constexpr int HPI = 32 / LP;                      // heads per pass of the warp
+    __shared__ float4 cs[kRopeThreads / 32][LP * 4];  // (cos, sin) of the token's pairs
     sm100::pdl_trigger();
     sm100::pdl_wait();
-    const int t0 = blockIdx.x * tile;
-    const int n = p.T - t0 < tile ? p.T - t0 : tile;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int u = lane % LP, hg = lane / LP;
     const int half = p.rot >> 1;
-    for (int i = threadIdx.x; i < n * half; i += kRopeThreads) {
-        const int t = i / half;
-        cs[i] = cos_sin(p, position_of(p, t0 + t), i - t * half);
-    }
-    if (p.append && threadIdx.x < n) crow[threadIdx.x] = cache_row(p, t0 + threadIdx.x);
-    __syncthreads();
-    const int u = threadIdx.x % LP;                   // this lane's 16 values of the head
-    const int units = p.D >> 4, runits = p.rot >> 4;
-    const int items = n * p.heads;
-    for (int it0 = 0; it0 < items; it0 += kRopeThreads / LP) {
-        const int idx = it0 + threadIdx.x / LP;
-        const int t = idx / p.heads;
-        Item<T> it;
-        const bool live = idx < items && item_of(p, t0 + t, idx - t * p.heads, p.append ? crow[t] : 0, it) && u < units;
-        // the lane's two vectors: the two sides of 8 pairs, or 16 values that only pass
-        const bool pairs = u < runits;
-        const int e0 = pairs && p.layout == ORTHRUS_ROPE_HALF ? 8 * u : 16 * u;
-        const int e1 = pairs && p.layout == ORTHRUS_ROPE_HALF ? half + 8 * u : 16 * u + 8;
-        float a[8], b[8];
-        if (live) {
-            load8(it.src + e0, a);
-            load8(it.src + e1, b);
-        }
-        if (p.q_norm || p.k_norm) {
-            float ss = 0.f;
-            if (live) {
+    const bool pairs = u < p.rot >> 4, mine = u < p.D >> 4;
+    const bool norm = p.q_norm || p.k_norm;
+    // the lane's two vectors: the two sides of 8 pairs, or 16 values that only pass
+    const int e0 = pairs && p.layout == ORTHRUS_ROPE_HALF ? 8 * u : 16 * u;
+    const int e1 = pairs && p.layout == ORTHRUS_ROPE_HALF ? half + 8 * u : 16 * u + 8;
+    const int64_t step = (int64_t)gridDim.x * (kRopeThreads / 32);
+    for (int64_t unit = (int64_t)blockIdx.x * (kRopeThreads / 32) + warp; unit < units; unit += step) {
+        const int t = (int)(unit / runs), h_lo = (int)(unit - (int64_t)t * runs) * run;
+        const int h_hi = h_lo + run < p.heads ? h_lo + run : p.heads;
+        const int pos = position_of(p, t);
+        const int64_t crow = p.append && h_hi > p.Hq ? cache_row(p, t) : 0;
+        float2 f[8];
+        for (int hb = h_lo; hb < h_hi; hb += U * HPI) {
+            Raw8<T> ra[U], rb[U];
+            Item<T> it[U];
+            bool live[U];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss += a[j] * a[j] + b[j] * b[j];
-            }
-#pragma unroll
-            for (int o = LP / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-            if (live && it.norm) {
-                const float inv = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-                float w[8];
-                load8(it.norm + e0, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] = a[j] * inv * w[j];
-                load8(it.norm + e1, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) b[j] = b[j] * inv * w[j];
-            }
-        }
-        if (!live) continue;
-        if (it.rotate && pairs) {
-            const float2 *f = cs + t * half + 8 * u;
-            if (p.layout == ORTHRUS_ROPE_HALF) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float x = a[j], y = b[j];
-                    a[j] = x * f[j].x - y * f[j].y;
-                    b[j] = y * f[j].x + x * f[j].y;
+            for (int i = 0; i < U; ++i) {
+                const int h = hb + i * HPI + hg;
+                live[i] = h < h_hi && mine && item_of(p, t, h, crow, it[i]);
+                if (live[i]) {
+                    ra[i] = load_raw(it[i].src + e0);
+                    rb[i] = load_raw(it[i].src + e1);
                 }
-            } else {
+            }
+            if (hb == h_lo) {
+                __syncwarp();                         // (the last unit's pairs have been read)
+                for (int i = lane; i < half; i += 32) reinterpret_cast<float2 *>(cs[warp])[i] = cos_sin(p, pos, i);
+                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float x = a[2 * j], y = a[2 * j + 1];
-                    a[2 * j] = x * f[j].x - y * f[j].y;
-                    a[2 * j + 1] = y * f[j].x + x * f[j].y;
-                    x = b[2 * j], y = b[2 * j + 1];
-                    b[2 * j] = x * f[4 + j].x - y * f[4 + j].y;
-                    b[2 * j + 1] = y * f[4 + j].x + x * f[4 + j].y;
+                    const float4 v = cs[warp][4 * u + j];
+                    f[2 * j] = make_float2(v.x, v.y);
+                    f[2 * j + 1] = make_float2(v.z, v.w);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float2 a[4], b[4];
+                if (live[i]) {
+                    unpack8<T>(ra[i], a);
+                    unpack8<T>(rb[i], b);
+                }
+                if (norm) {
+                    float ss = 0.f;
+                    if (live[i]) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            ss += a[j].x * a[j].x + a[j].y * a[j].y + b[j].x * b[j].x + b[j].y * b[j].y;
+                    }
+#pragma unroll
+                    for (int o = LP / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                    if (live[i] && it[i].norm) {
+                        const float inv = 1.0f / sqrtf(ss / (float)p.D + p.eps);
+                        float2 w[4];
+                        unpack8<T>(load_raw(it[i].norm + e0), w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) a[j] = make_float2(a[j].x * inv * w[j].x, a[j].y * inv * w[j].y);
+                        unpack8<T>(load_raw(it[i].norm + e1), w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) b[j] = make_float2(b[j].x * inv * w[j].x, b[j].y * inv * w[j].y);
+                    }
+                }
+                if (!live[i]) continue;
+                if (it[i].rotate && pairs) {
+                    if (p.layout == ORTHRUS_ROPE_HALF) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = a[j], y = b[j], f0 = f[2 * j], f1 = f[2 * j + 1];
+                            a[j] = make_float2(x.x * f0.x - y.x * f0.y, x.y * f1.x - y.y * f1.y);
+                            b[j] = make_float2(y.x * f0.x + x.x * f0.y, y.y * f1.x + x.y * f1.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = a[j], y = b[j];
+                            a[j] = make_float2(x.x * f[j].x - x.y * f[j].y, x.y * f[j].x + x.x * f[j].y);
+                            b[j] = make_float2(y.x * f[4 + j].x - y.y * f[4 + j].y, y.y * f[4 + j].x + y.x * f[4 + j].y);
+                        }
+                    }
+                }
+                store8(it[i].dst + e0, a);
+                store8(it[i].dst + e1, b);
+            }
         }
-        store8(it.dst + e0, a);
-        store8(it.dst + e1, b);
     }
 }
 
@@ -249,26 +268,36 @@ template <typename T> __global__ void __launch_bounds__(kRopeThreads) rope_any_k
     }
 }
 
+template <typename T, int LP> cudaError_t launch_rope_v(const RopeArgs &p, int sms, cudaStream_t st)
+{
+    // Heads per warp: all of a token's (one set of angles) once the tokens alone
+    // fill the SMs' warps, else as few passes as it takes to fill them.
+    constexpr int U = sizeof(T) == 2 ? 4 : 2, HPI = 32 / LP;
+    const int64_t want = 16ll * sms;                  // warps
+    const int passes = (p.heads + HPI - 1) / HPI;
+    int64_t runs = (want + p.T - 1) / p.T;
+    if (runs > passes) runs = passes;
+    const int run = (int)((passes + runs - 1) / runs) * HPI;
+    runs = (p.heads + run - 1) / run;
+    const int64_t units = (int64_t)p.T * runs, blocks = (units + 7) / 8, most = 8ll * sms;
+    return launch_pdl(rope_kernel<T, LP, U>, dim3((unsigned)(blocks < most ? blocks : most)), kRopeThreads, 0, st, p, run,
+                      (int)runs, units);
+}
+
 template <typename T> cudaError_t launch_rope_t(const RopeArgs &p, bool vec, int sms, cudaStream_t st)
 {
     if (!vec) {
         const int64_t blocks = ((int64_t)p.T * p.heads + 7) / 8, most = 8ll * sms;
         return launch_pdl(rope_any_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), kRopeThreads, 0, st, p);
     }
-    // one token per block while that leaves SMs idle, else up to four (the
-    // (cos, sin) pairs of four tokens fill the block's threads once)
-    int tile = p.T / (2 * sms);
-    tile = tile < 1 ? 1 : tile > 4 ? 4 : tile;
-    const dim3 grid((unsigned)((p.T + tile - 1) / tile));
-    const size_t smem = (size_t)tile * (p.rot / 2) * sizeof(float2);
     int lp = 1;
     while (lp * 16 < p.D) lp *= 2;
     switch (lp) {
-    case 1: return launch_pdl(rope_kernel<T, 1>, grid, kRopeThreads, smem, st, p, tile);
-    case 2: return launch_pdl(rope_kernel<T, 2>, grid, kRopeThreads, smem, st, p, tile);
-    case 4: return launch_pdl(rope_kernel<T, 4>, grid, kRopeThreads, smem, st, p, tile);
-    case 8: return launch_pdl(rope_kernel<T, 8>, grid, kRopeThreads, smem, st, p, tile);
-    default: return launch_pdl(rope_kernel<T, 16>, grid, kRopeThreads, smem, st, p, tile);
+    case 1: return launch_rope_v<T, 1>(p, sms, st);
+    case 2: return launch_rope_v<T, 2>(p, sms, st);
+    case 4: return launch_rope_v<T, 4>(p, sms, st);
+    case 8: return launch_rope_v<T, 8>(p, sms, st);
+    default: return launch_rope_v<T, 16>(p, sms, st);
     }
 }
 
