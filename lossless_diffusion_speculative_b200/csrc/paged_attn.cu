@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     float2 *comb_ml = reinterpret_cast<float2 *>(smem + L::kRing);   // [warp][row]
     volatile uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::kRing + L::kML);
     int *pre = reinterpret_cast<int *>(smem + L::kFixed);            // [B + 1]
-    __shared__ int flag;
+    __shared__ int flag, blocks;
+    __shared__ float2 seg_ml[kRows];                                 // a join's maxima and 1 / sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int segs = p.Hkv * p.HG;
     pdl_trigger();
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
 
     // ---- the flat tile order: exclusive prefix of the sequences' tile counts
     if (warp == 0) {
-        int run = 0;
+        int run = 0, n_max = 0, n_min = 0x7fffffff, held = 0;     // tiles per segment, sequences with any
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
             int n = b < p.B ? (visible(p, b, blockIdx.x == 0) + kTile - 1) / kTile : 0;
@@ -148,8 +149,29 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
             }
             if (b < p.B) pre[b] = run + x - n;
             run += __shfl_sync(~0u, x, 31);
+            if (n) {
+                n_max = n > n_max ? n : n_max;
+                n_min = n < n_min ? n : n_min;
+                ++held;
+            }
         }
-        if (lane == 0) pre[p.B] = run;
+        n_max = __reduce_max_sync(~0u, n_max);
+        n_min = __reduce_min_sync(~0u, n_min);
+        held = __reduce_add_sync(~0u, held);
+        if (lane == 0) {
+            pre[p.B] = run;
+            // Blocks with work.  Segments of equal length take whole blocks each,
+            // so that no block straddles two, and one block where a join
+            // (~3 us of dependent steps) would cost more than the tiles it
+            // spreads (~0.4 us each).
+            const int64_t total = (int64_t)run * segs, seg = (int64_t)held * segs;
+            int64_t P = total < gridDim.x ? total : gridDim.x;
+            if (n_max == n_min && seg <= gridDim.x) {
+                const int64_t k = gridDim.x / seg;
+                P = seg * (n_max <= 8 ? 1 : k < n_max ? k : n_max);
+            }
+            blocks = (int)P;
+        }
     }
     __syncthreads();
     const int64_t total = (int64_t)pre[p.B] * segs;
@@ -158,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)
         if (pre[b + 1] == pre[b])
             for (int i = threadIdx.x; i < p.Hq * D; i += kThreads) out[(size_t)b * p.Hq * D + i] = from_f32<T>(0.f);
-    const int64_t P = total < gridDim.x ? total : gridDim.x;         // blocks with work
+    const int64_t P = blocks;
     if (blockIdx.x >= P) return;
     auto range = [&](int64_t c) { return c * total / P; };
     const int64_t lo = range(blockIdx.x), hi = range(blockIdx.x + 1);
@@ -244,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     // ---- per-segment state
     uint32_t qf[D / 16][4];
     float o[D / 8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    auto begin = [&]() {
+    auto load_q = [&]() {
         const int g = cur.g / p.HG, h0 = (cur.g - g * p.HG) * kRows;
         const int r0 = h0 + (lane >> 2), r1 = r0 + 8;
         const T *q = static_cast<const T *>(p.q) + ((size_t)cur.b * p.Hq + g * p.G) * D + (lane & 3) * 2;
@@ -255,6 +277,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
             qf[k][2] = r0 < p.G ? *reinterpret_cast<const uint32_t *>(q + r0 * D + k * 16 + 8) : 0u;
             qf[k][3] = r1 < p.G ? *reinterpret_cast<const uint32_t *>(q + r1 * D + k * 16 + 8) : 0u;
         }
+    };
+    auto clear = [&]() {
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -262,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
         m0 = m1 = -INFINITY;
         l0 = l1 = 0.f;
     };
-    begin();
+    load_q();
+    clear();
 
     int stage = 0;
     for (int64_t x = lo; x < hi; ++x) {
@@ -348,12 +373,17 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
         cp_commit();
 
         if (cur.t + 1 == cur.n || x + 1 == hi) {   // the block leaves this segment
+            const Pos seg_ = cur;
+            if (x + 1 < hi) {
+                advance(cur);
+                load_q();                          // (on its way during the rest)
+            }
 #pragma unroll
             for (int d = 1; d < 4; d <<= 1) {
                 l0 += __shfl_xor_sync(~0u, l0, d);
                 l1 += __shfl_xor_sync(~0u, l1, d);
             }
-            const int rowsG = p.G - (cur.g % p.HG) * kRows, rows = rowsG < kRows ? rowsG : kRows;
+            const int rowsG = p.G - (seg_.g % p.HG) * kRows, rows = rowsG < kRows ? rowsG : kRows;
             const int r0 = lane >> 2, r1 = r0 + 8;
             // the stage just read holds O now (its next load is issued an iteration
             // later); 8-value chunk i of row r sits at i ^ (r & 7)
@@ -372,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                 comb_ml[warp * kRows + r1] = make_float2(m1, l1);
             }
             __syncthreads();
-            const int64_t s0 = (int64_t)pre[cur.b] * segs + (int64_t)cur.g * cur.n;      // the segment's flat tiles
-            const bool whole = lo <= s0 && hi >= s0 + cur.n;
-            const int g = cur.g / p.HG, h0 = (cur.g - g * p.HG) * kRows;
-            T *dst = out + ((size_t)cur.b * p.Hq + g * p.G + h0) * D;
+            const int64_t s0 = (int64_t)pre[seg_.b] * segs + (int64_t)seg_.g * seg_.n;      // the segment's flat tiles
+            const bool whole = lo <= s0 && hi >= s0 + seg_.n;
+            const int g = seg_.g / p.HG, h0 = (seg_.g - g * p.HG) * kRows;
+            T *dst = out + ((size_t)seg_.b * p.Hq + g * p.G + h0) * D;
             const size_t slot = 2 * (size_t)blockIdx.x + (lo < s0 ? 1 : 0);
             for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -404,8 +434,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
             }
             if (!whole) {
                 // blocks [c0, c1] hold the segment; the last to arrive joins it
-                const int c_first = (int)(((s0 + 1) * P - 1) / total), c_last = (int)(((s0 + cur.n) * P - 1) / total);
-                const int seg = cur.b * segs + cur.g, n = c_last - c_first + 1;
+                const int c_first = (int)(((s0 + 1) * P - 1) / total), c_last = (int)(((s0 + seg_.n) * P - 1) / total);
+                const int seg = seg_.b * segs + seg_.g, n = c_last - c_first + 1;
                 __syncthreads();                   // every partial store of the block, before the release
                 if (threadIdx.x == 0) {
                     const int old = counter_fetch_add_acq_rel(p.counters + seg, 1);
@@ -414,36 +444,47 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                 }
                 __syncthreads();
                 if (flag) {
-                    auto slot_of = [&](int j) {
-                        const int64_t c = c_first + j;
-                        return 2 * (size_t)c + (range(c) < s0 ? 1 : 0);
-                    };
+                    // (the first block may have come to the segment from another one;
+                    // every other block's range begins inside it)
+                    const size_t slot0 = 2 * (size_t)c_first + (range(c_first) < s0 ? 1 : 0);
+                    auto slot_of = [&](int j) { return j ? 2 * (size_t)(c_first + j) : slot0; };
+                    // a row's maximum and sum: a warp per row, its lanes over the partials
+                    for (int r = warp; r < rows; r += kWarps) {
+                        float M = -INFINITY, l = 0.f;
+                        for (int j = lane; j < n; j += 32) {
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) * kRows + r) * 2));
+                            const float m = fmaxf(M, ml.x);
+                            if (m != -INFINITY) l = l * fast_exp2(M - m) + ml.y * fast_exp2(ml.x - m);
+                            M = m;
+                        }
+                        float A = M;
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) A = fmaxf(A, __shfl_xor_sync(~0u, A, d));
+                        l = M == -INFINITY ? 0.f : l * fast_exp2(M - A);
+#pragma unroll
+                        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+                        if (lane == 0)
+                            seg_ml[r] = make_float2(A == -INFINITY ? 0.f : A, l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l);
+                    }
+                    __syncthreads();
                     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
                         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-                        float M = -INFINITY, l = 0.f;
+                        const float E = seg_ml[r].x, inv = seg_ml[r].y;
                         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int j = 0; j < n; ++j)
-                            M = fmaxf(M, __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) * kRows + r) * 2)).x);
-                        const float E = M == -INFINITY ? 0.f : M;
+#pragma unroll 8
                         for (int j = 0; j < n; ++j) {
                             const size_t sl = slot_of(j) * kRows + r;
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + sl * 2));
+                            const float f = fast_exp2(__ldcg(p.part_ml + sl * 2) - E);
                             const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + sl * D + d));
-                            const float f = fast_exp2(ml.x - E);
-                            l += ml.y * f;
                             a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
                         }
-                        const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;
                         *reinterpret_cast<uint2 *>(dst + r * D + d) =
                             make_uint2(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv));
                     }
                 }
             }
             __syncthreads();                       // the combine buffer and the flag are free again
-            if (x + 1 < hi) {
-                advance(cur);
-                begin();
-            }
+            clear();
         } else {
             ++cur.t;
         }
