@@ -11,10 +11,10 @@
 // 48 such instructions per 16 keys x 128 dims (8 KB) against the ~350 cycles
 // the SM's share of HBM needs to deliver them.
 //
-// Work split: every sequence's keys are cut into tiles of 64; the tiles of all
+// Work split: every sequence's keys are cut into tiles of 64 (128 for D = 64); the tiles of all
 // (sequence, KV head, group of 16 heads) segments are laid end to end and cut
 // into equal contiguous ranges, one per block, computed on the device from
-// ctx_lens.  Each of the block's four warps takes 16 keys of a tile and runs its
+// ctx_lens.  Each of the block's four warps takes a quarter of a tile and runs its
 // own cp.async ring and its own running maximum and sum (no block-wide barrier
 // inside a segment); the four are combined through shared memory when the block
 // leaves a segment.  A segment that spans blocks is joined by the last of them
@@ -40,8 +40,6 @@ using namespace sm100;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStrip = 16;                       // keys per warp and tile
-constexpr int kTile = kWarps * kStrip;
 constexpr int kRows = 16;                        // query heads per segment (the MMA's M)
 constexpr int kMaxB = 4096;
 constexpr float kLazy = 8.f;                     // log2 units
@@ -108,14 +106,17 @@ struct Pos {
 // a segment's end, the rings' key masks, and after them the first flat tile of
 // every sequence (prefix, in tiles of one segment).
 template <int D> struct Layout {
+    // keys per warp and tile: 8 KB of keys and values, so that a tile's fixed
+    // costs (lookup, softmax, signals) weigh the same for heads of 64 and 128
+    static constexpr int kStrip = D == 64 ? 32 : 16, kTile = kWarps * kStrip;
     static constexpr int kStripBytes = kStrip * D * 2;               // keys (or values) of a strip
-    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kStages = 3;
     static constexpr int kRing = kWarps * kStages * 2 * kStripBytes;
     static constexpr int kML = kWarps * kRows * 2 * 4;               // m, l per warp and row
     static constexpr int kMask = kWarps * kStages * 4;
     static constexpr int kFixed = kRing + kML + kMask;
     // a warp's O of 16 rows takes the place of the strip it has just read
-    static_assert(2 * kStripBytes == kRows * D * 4, "O fits a stage");
+    static_assert(2 * kStripBytes >= kRows * D * 4, "O fits a stage");
 };
 
 // (blocks of D = 64 and 128 fit twice into an SM)
@@ -123,7 +124,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(const Args p)
 {
     using L = Layout<D>;
-    constexpr int kStages = L::kStages, CH = D / 8;                  // 16-byte chunks of a row
+    constexpr int kStages = L::kStages, kStrip = L::kStrip, kTile = L::kTile;
+    constexpr int CH = D / 8;                                        // 16-byte chunks of a row
+    constexpr int NS = kStrip / 16;                                  // 16-key steps of a strip
     extern __shared__ __align__(128) uint8_t smem[];
     float2 *comb_ml = reinterpret_cast<float2 *>(smem + L::kRing);   // [warp][row]
     volatile uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::kRing + L::kML);
@@ -162,13 +165,13 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
             pre[p.B] = run;
             // Blocks with work.  Segments of equal length take whole blocks each,
             // so that no block straddles two, and one block where a join
-            // (~3 us of dependent steps) would cost more than the tiles it
-            // spreads (~0.4 us each).
+            // (~3.5 us of dependent steps) would cost more than the tiles it
+            // spreads (~1.1 us each, measured on one sequence).
             const int64_t total = (int64_t)run * segs, seg = (int64_t)held * segs;
             int64_t P = total < gridDim.x ? total : gridDim.x;
             if (n_max == n_min && seg <= gridDim.x) {
                 const int64_t k = gridDim.x / seg;
-                P = seg * (n_max <= 8 ? 1 : k < n_max ? k : n_max);
+                P = seg * (n_max <= 3 ? 1 : k < n_max ? k : n_max);
             }
             blocks = (int)P;
         }
@@ -219,13 +222,13 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     const T *kp = static_cast<const T *>(p.k_pages), *vp = static_cast<const T *>(p.v_pages);
     Pos iss = cur;
     int64_t issued = lo;
-    // row offset (in rows of D) of the strip's key `lane & 15`, -1 where there is none
+    // row offset (in rows of D) of the strip's key `lane`, -1 where there is none
     int64_t next_row = -1;
     auto look_up = [&]() {
         next_row = -1;
         if (issued < hi) {
-            const int j = iss.t * kTile + warp * kStrip + (lane & 15);
-            if (j < iss.len) {
+            const int j = iss.t * kTile + warp * kStrip + lane;
+            if (lane < kStrip && j < iss.len) {
                 const int e = j / p.page_size;
                 const int page = p.block_table[(int64_t)iss.b * p.max_pages + e];
                 if (page >= 0 && page < p.num_pages)
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     look_up();
     auto issue = [&](int stage) {
         const uint32_t dk = ring + stage * 2 * L::kStripBytes, dv = dk + L::kStripBytes;
-        const uint32_t m = __ballot_sync(~0u, next_row >= 0) & 0xffffu;
+        const uint32_t m = __ballot_sync(~0u, next_row >= 0);
         if (lane == 0) masks[warp * kStages + stage] = m;
         if (m) {
 #pragma unroll
@@ -296,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
         const uint32_t mask = masks[warp * kStages + stage];
         const uint32_t sk = ring + stage * 2 * L::kStripBytes, sv = sk + L::kStripBytes;
         if (mask) {
-            float s[2][4];
+            float s[2 * NS][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2 * NS; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
             {
@@ -306,21 +309,26 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                 const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    uint32_t b[4];
-                    ldsm4(b, sk + r * D * 2 + (((2 * k + cc) ^ (r & 7)) << 4));
-                    mma<T>(s[0], qf[k], b[0], b[1]);
-                    mma<T>(s[1], qf[k], b[2], b[3]);
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        uint32_t b[4];
+                        ldsm4(b, sk + (i * 16 + r) * D * 2 + (((2 * k + cc) ^ (r & 7)) << 4));
+                        mma<T>(s[2 * i], qf[k], b[0], b[1]);
+                        mma<T>(s[2 * i + 1], qf[k], b[2], b[3]);
+                    }
                 }
             }
-            // columns of this thread: keys 2 (lane & 3) + {0, 1} of each half
+            // columns of this thread: keys 2 (lane & 3) + {0, 1} of each 8
             const uint32_t mk = mask >> ((lane & 3) * 2);
+            float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2 * NS; ++i) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     s[i][j] = (mk >> (8 * i + (j & 1))) & 1u ? s[i][j] * p.scale_log2 : -INFINITY;
-            float a0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-            float a1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+                a0 = fmax3(a0, s[i][0], s[i][1]);
+                a1 = fmax3(a1, s[i][2], s[i][3]);
+            }
 #pragma unroll
             for (int d = 1; d < 4; d <<= 1) {
                 a0 = fmaxf(a0, __shfl_xor_sync(~0u, a0, d));
@@ -343,9 +351,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
             }
             // a row whose scores so far are all -inf keeps the weights at zero
             const float e0 = m0 == -INFINITY ? 0.f : m0, e1 = m1 == -INFINITY ? 0.f : m1;
-            uint32_t hi_[4], lo_[4];
+            uint32_t hi_[NS][4], lo_[NS][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2 * NS; ++i) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float e = h ? e1 : e0;
@@ -353,20 +361,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                     if (h) l1 += x0 + x1; else l0 += x0 + x1;
                     const uint32_t w = pack2<T>(x0, x1);
                     const float2 back = unpack2<T>(w);
-                    hi_[2 * i + h] = w;
-                    lo_[2 * i + h] = pack2<T>(x0 - back.x, x1 - back.y);
+                    hi_[i / 2][2 * (i & 1) + h] = w;
+                    lo_[i / 2][2 * (i & 1) + h] = pack2<T>(x0 - back.x, x1 - back.y);
                 }
             }
             // matrices: dims lo | keys 0-7, 8-15, then dims hi | keys 0-7, 8-15
             const int r = lane & 15, cc = lane >> 4;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
-                uint32_t b[4];
-                ldsm4_t(b, sv + r * D * 2 + (((2 * d + cc) ^ (r & 7)) << 4));
-                mma<T>(o[2 * d], hi_, b[0], b[1]);
-                mma<T>(o[2 * d + 1], hi_, b[2], b[3]);
-                mma<T>(o[2 * d], lo_, b[0], b[1]);
-                mma<T>(o[2 * d + 1], lo_, b[2], b[3]);
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    uint32_t b[4];
+                    ldsm4_t(b, sv + (i * 16 + r) * D * 2 + (((2 * d + cc) ^ (r & 7)) << 4));
+                    mma<T>(o[2 * d], hi_[i], b[0], b[1]);
+                    mma<T>(o[2 * d + 1], hi_[i], b[2], b[3]);
+                    mma<T>(o[2 * d], lo_[i], b[0], b[1]);
+                    mma<T>(o[2 * d + 1], lo_[i], b[2], b[3]);
+                }
             }
         }
         issue((stage + kStages - 1) % kStages);
@@ -580,7 +591,7 @@ extern "C" int orthrus_paged_attn(orthrus_dtype dtype, const void *q, const void
     if (dtype != ORTHRUS_BF16 && dtype != ORTHRUS_F16) return dtype == ORTHRUS_F32 ? ORTHRUS_ERR_UNSUPPORTED : ORTHRUS_ERR_ARG;
     if (!paged::shape_supported(B, Hq, D)) return ORTHRUS_ERR_UNSUPPORTED;
     if ((int64_t)max_pages * page_size > (1ll << 31) - 128 ||
-        ((int64_t)max_pages * page_size / paged::kTile + 1) * B >= (1ll << 31))
+        ((int64_t)max_pages * page_size / 64 + 1) * B >= (1ll << 31))
         return ORTHRUS_ERR_UNSUPPORTED;          // (positions and the tile prefix are 32-bit)
     if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out | (uintptr_t)workspace) & 15u)
         return ORTHRUS_ERR_ALIGN;
