@@ -119,6 +119,56 @@ template <int D> struct Layout {
     static_assert(2 * kStripBytes >= kRows * D * 4, "O fits a stage");
 };
 
+// Output of a segment from its n partials, weighted by the rows' joint maxima
+// and 1 / sums in `ml`: Q four-value pieces per thread at a time, 16 loads in
+// flight.  Partial 0 sits in slot0, partial j in slot1 + 2 (j - 1).
+template <typename T, int D, int Q>
+__device__ __forceinline__ void join_pieces(const Args &p, T *dst, int items, int n, size_t slot0, size_t slot1,
+                                            const float2 *ml)
+{
+    for (int i0 = threadIdx.x; i0 < items; i0 += Q * kThreads) {
+        float4 a[Q];
+        float E[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int i = i0 + q * kThreads;
+            a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            E[q] = i < items ? ml[i / (D / 4)].x : 0.f;
+        }
+#pragma unroll 16 / Q
+        for (int j = 0; j < n; ++j) {
+            const size_t slot = (j ? slot1 + 2 * (j - 1) : slot0) * kRows;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = i0 + q * kThreads;
+                if (i < items) {
+                    const size_t sl = slot + i / (D / 4);
+                    const float f = fast_exp2(__ldcg(p.part_ml + sl * 2) - E[q]);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + sl * D + i % (D / 4) * 4));
+                    a[q].x += v.x * f, a[q].y += v.y * f, a[q].z += v.z * f, a[q].w += v.w * f;
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int i = i0 + q * kThreads;
+            if (i < items) {
+                const int r = i / (D / 4), d = i % (D / 4) * 4;
+                const float inv = ml[r].y;
+                *reinterpret_cast<uint2 *>(dst + r * D + d) =
+                    make_uint2(pack2<T>(a[q].x * inv, a[q].y * inv), pack2<T>(a[q].z * inv, a[q].w * inv));
+            }
+        }
+    }
+}
+template <typename T, int D>
+__device__ __forceinline__ void join_rows(const Args &p, T *dst, int rows, int n, size_t slot0, size_t slot1, const float2 *ml)
+{
+    const int items = rows * (D / 4);
+    if (items <= kThreads) join_pieces<T, D, 1>(p, dst, items, n, slot0, slot1, ml);
+    else join_pieces<T, D, 4>(p, dst, items, n, slot0, slot1, ml);
+}
+
 // (blocks of D = 64 and 128 fit twice into an SM)
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(const Args p)
@@ -458,40 +508,31 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                     // (the first block may have come to the segment from another one;
                     // every other block's range begins inside it)
                     const size_t slot0 = 2 * (size_t)c_first + (range(c_first) < s0 ? 1 : 0);
-                    auto slot_of = [&](int j) { return j ? 2 * (size_t)(c_first + j) : slot0; };
-                    // a row's maximum and sum: a warp per row, its lanes over the partials
-                    for (int r = warp; r < rows; r += kWarps) {
+                    auto slot_of = [&](int j) { return (j ? 2 * (size_t)(c_first + j) : slot0) * kRows; };
+                    // the rows' maxima and sums: eight lanes per row, over the partials
+                    {
+                        const int r = threadIdx.x >> 3;
                         float M = -INFINITY, l = 0.f;
-                        for (int j = lane; j < n; j += 32) {
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) * kRows + r) * 2));
-                            const float m = fmaxf(M, ml.x);
-                            if (m != -INFINITY) l = l * fast_exp2(M - m) + ml.y * fast_exp2(ml.x - m);
-                            M = m;
+                        if (r < rows) {
+#pragma unroll 4
+                            for (int j = threadIdx.x & 7; j < n; j += 8) {
+                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) + r) * 2));
+                                const float m = fmaxf(M, ml.x);
+                                if (m != -INFINITY) l = l * fast_exp2(M - m) + ml.y * fast_exp2(ml.x - m);
+                                M = m;
+                            }
                         }
                         float A = M;
 #pragma unroll
-                        for (int d = 16; d; d >>= 1) A = fmaxf(A, __shfl_xor_sync(~0u, A, d));
+                        for (int d = 4; d; d >>= 1) A = fmaxf(A, __shfl_xor_sync(~0u, A, d));
                         l = M == -INFINITY ? 0.f : l * fast_exp2(M - A);
 #pragma unroll
-                        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-                        if (lane == 0)
+                        for (int d = 4; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+                        if ((threadIdx.x & 7) == 0)               // (a sum that is not a number stays one)
                             seg_ml[r] = make_float2(A == -INFINITY ? 0.f : A, l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l);
                     }
                     __syncthreads();
-                    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
-                        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-                        const float E = seg_ml[r].x, inv = seg_ml[r].y;
-                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                        for (int j = 0; j < n; ++j) {
-                            const size_t sl = slot_of(j) * kRows + r;
-                            const float f = fast_exp2(__ldcg(p.part_ml + sl * 2) - E);
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + sl * D + d));
-                            a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
-                        }
-                        *reinterpret_cast<uint2 *>(dst + r * D + d) =
-                            make_uint2(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv));
-                    }
+                    join_rows<T, D>(p, dst, rows, n, slot0, 2 * (size_t)(c_first + 1), seg_ml);
                 }
             }
             __syncthreads();                       // the combine buffer and the flag are free again
