@@ -439,7 +439,7 @@ int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaS
     const uint64_t str[1] = {(uint64_t)p.K}, ostr[1] = {(uint64_t)p.N * sizeof(T)};
     const uint64_t dx[2] = {(uint64_t)p.K, (uint64_t)p.M}, dy[2] = {(uint64_t)p.K, (uint64_t)p.N},
                    dz[2] = {(uint64_t)p.N * sizeof(T), (uint64_t)p.M};
-    const uint32_t bx[2] = {128, 128}, by[2] = {128, 128};
+    const uint32_t bx[2] = {128, 128}, by[2] = {128, 64};
     if (!encode_u8_sw128(&mp.x, 2, a, dx, str, bx) || !encode_u8_sw128(&mp.y, 2, w, dy, str, by)) return ORTHRUS_ERR_LAUNCH;
     if (p.vec) {
         if (!encode_u8_sw128(&mp.o, 2, p.out, dz, ostr, bx)) return ORTHRUS_ERR_LAUNCH;

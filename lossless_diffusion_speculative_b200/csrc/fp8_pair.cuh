@@ -6,10 +6,15 @@
 //   - the scales.  Each k-block's sums are read from TMEM and added, scaled, to
 //     fp32 registers: eight warps, a token row per lane, 128 columns each (half
 //     of the register file holds the CTA's 128 x 256 sums).  A buffer's round
-//     trip (multiply, signal, read, signal back) is longer than two blocks'
-//     multiplication, so the two column halves have two TMEM buffers each and
-//     are multiplied, signalled and freed separately: 256 + ~900 cycles per
-//     two blocks of a half, against 512 + ~900 for both halves together.
+//     trip (multiply, signal, read and add, signal back) takes ~1500 cycles
+//     against the 512 of a block's multiplication, so the two column halves
+//     have two TMEM buffers each and are multiplied, signalled and freed
+//     separately (706k cycles a call at 8192 x 12288 x 4096 with both halves
+//     together, 610k apart; the multiplications alone are 340k).  The issuing
+//     thread shares its scheduler with two epilogue warps, so what it and they
+//     issue counts: the sums use two-element FMAs (one-element ones: 746k) on
+//     chunks of 16 columns (32: 749k), no votes between signals, one issuing
+//     thread (one per half: 770k).
 //   - the row scales lie [row][k-block] in memory, a line per row: a warp of
 //     its own copies 16 k-blocks of all rows at a time, coalesced along k.
 //     (Loaded by the epilogue's lanes, a row each, the same copies took the L1
@@ -28,7 +33,7 @@ constexpr int kScaleGroup = 16;                       // k-blocks whose scales a
 constexpr int kScalePitch = 129;                      // row scales [k-block][row], padded for the copies' banks
 
 struct PairMaps {
-    CUtensorMap x, y, o;                 // a: box 128 x 128; w: box 128 x 128; out: box 128 bytes x 128 rows
+    CUtensorMap x, y, o;                 // a: box 128 x 128; w: box 128 x 64; out: box 128 bytes x 128 rows
 };
 
 struct PairConf {
@@ -37,18 +42,19 @@ struct PairConf {
     static constexpr int out_half = 32 * 1024;                        // staging of one column half: two boxes
     static constexpr int out = nst * stage;
     static constexpr int bars = out + 2 * out_half;
-    // stage full / empty, TMEM buffer full / empty, scale group full / empty, drain
-    static constexpr int nbars = 2 * nst + 4 + 4 + 1;
+    // stage full / empty, TMEM buffer [half][2] full / empty, scale group full / empty, drain
+    static constexpr int nbars = 2 * nst + 8 + 4 + 1;
     static constexpr int sa = (bars + nbars * 8 + 16 + 15) & ~15;     // [2][16][129] row scales
     static constexpr int sw = sa + 2 * kScaleGroup * kScalePitch * 4; // [2][2 halves][16] weight scales
     static constexpr int total = sw + 2 * 2 * kScaleGroup * 4 + 1024;
     static_assert(total <= 227 * 1024 && nst == 4, "shared memory; the MMA loop's parities");
 };
 
-// Token tiles first, in strips of 8 tiles, so that the tiles in flight share operands in L2.
+// Token tiles first, in strips of 32, so that the pairs at work share few weight
+// tiles and all token rows come from L2 (strips of 8: 431 us sustained, 32: 420).
 __device__ __forceinline__ void pair_tile(const Args &p, int t, int &x, int &y)
 {
-    constexpr int G = 8;
+    constexpr int G = 32;
     const int strip = t / (G * p.tiles_y), r = t - strip * G * p.tiles_y;
     const int h = p.tiles_x - strip * G < G ? p.tiles_x - strip * G : G;
     y = r / h;
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sm = smem_raw + (base - raw);
     const uint32_t b_full = base + C::bars, b_empty = b_full + 8 * C::nst, b_tfull = b_empty + 8 * C::nst,
-                   b_tempty = b_tfull + 16, b_sfull = b_tempty + 16, b_sempty = b_sfull + 16, b_drain = b_sempty + 16;
+                   b_tempty = b_tfull + 32, b_sfull = b_tempty + 32, b_sempty = b_sfull + 16, b_drain = b_sempty + 16;
     volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::bars + C::nbars * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -93,9 +99,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(b_tfull + 8 * i, 1);
-            mbar_init(b_tempty + 8 * i, 2 * kEpiWarps);               // the warps of both CTAs
+            mbar_init(b_tempty + 8 * i, kEpiWarps);                   // four warps of both CTAs
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(b_sfull + 8 * i, 1);
             mbar_init(b_sempty + 8 * i, kEpiWarps);
         }
@@ -125,8 +133,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     if (warp < kEpiWarps) {
         constexpr int CPT = kPairN / 2;
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * CPT;
-        const uint32_t lead_tempty = map_to_rank(b_tempty, 0);
+        const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 2 * CPT;
+        const uint32_t tfull = b_tfull + 16 * half, lead_tempty = map_to_rank(b_tempty + 16 * half, 0);
         const float *sa = reinterpret_cast<const float *>(sm + C::sa) + row;
         const float *sw = reinterpret_cast<const float *>(sm + C::sw) + half * kScaleGroup;
         // staging of this half: boxes of 128 rows x 128 bytes, 16-byte chunks swizzled by the row
@@ -144,24 +152,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             for (int kb = 0; kb < p.nkb; ++kb, ++it) {
                 const int in = kb % kScaleGroup;
                 if (in == 0) {
-                    if (ok) ok = __all_sync(~0u, wait_bar_near(b_sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag, p.status));
+                    ok &= wait_bar_near(b_sfull + 8 * (g & 1), (g >> 1) & 1, abort_flag, p.status);
+                    __syncwarp();
                     ++g;
                 }
                 const int gb = (g - 1) & 1, buf = it & 1;
-                if (!ok) continue;
                 const float sc = sa[(gb * kScaleGroup + in) * kScalePitch] * sw[gb * 2 * kScaleGroup + in];
                 const float2 s2 = make_float2(sc, sc);
-                ok = __all_sync(~0u, wait_bar_near(b_tfull + 8 * buf, (it >> 1) & 1, abort_flag, p.status));
-                if (!ok) continue;
+                // (no vote here: after an abort the warp goes on with what it reads
+                // and leaves at the tile's end)
+                ok &= wait_bar_near(tfull + 8 * buf, (it >> 1) & 1, abort_flag, p.status);
+                __syncwarp();
                 tc_fence_after();
                 // two chunks of 16 columns: one on its way while the other is added
                 uint32_t v[2][16];
-                tmem_ld16(t_row + buf * kPairN, v[0]);
+                tmem_ld16(t_row + buf * CPT, v[0]);
 #pragma unroll
                 for (int c = 0; c < CPT; c += 16) {
                     tmem_wait_ld();
                     if (c + 16 < CPT) {
-                        tmem_ld16(t_row + buf * kPairN + c + 16, v[(c / 16 + 1) & 1]);
+                        tmem_ld16(t_row + buf * CPT + c + 16, v[(c / 16 + 1) & 1]);
                     } else {                                          // all read: the buffer is free
                         tc_fence_before();
                         __syncwarp();
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
             for (int t = pair; t < tiles && ok; t += pairs) {
                 int x, y;
                 pair_tile(p, t, x, y);
-                const int m0 = x * 256 + rank * 128, n0 = y * kPairN + rank * 128;
+                const int m0 = x * 256 + rank * 128, n0 = y * kPairN + rank * 64;
 #pragma unroll 1
                 for (int kb = 0; kb < p.nkb; ++kb, ++it) {
                     const int st = it % C::nst, n = it / C::nst;
@@ -249,6 +259,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                     if (rank == 0) mbar_expect_tx(b_full + 8 * st, 2 * C::stage);
                     tma_load_2d_pair(dst, &mp.x, full, kb * 128, m0, keep);
                     tma_load_2d_pair(dst + kXBytes, &mp.y, full, kb * 128, n0, keep);
+                    tma_load_2d_pair(dst + kXBytes + 8192, &mp.y, full, kb * 128, n0 + 128, keep);
                 }
             }
             if (!ok && rank == 0) {                                   // abort: let both CTAs' copies in flight land
@@ -262,7 +273,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     } else if (warp == kEpiWarps + 1) {
         // ---- MMA: the even CTA issues for both
         if (rank == 0 && elect_one()) {
-            constexpr uint32_t idesc = instr_desc_e4m3(256, kPairN);
+            constexpr uint32_t idesc = instr_desc_e4m3(256, kPairN / 2);
             const int steps = (tiles - pair + pairs - 1) / pairs * p.nkb;
             const uint64_t ax0 = smem_desc(base, 16, 1024), ay0 = smem_desc(base + kXBytes, 16, 1024);
             bool ok = true;
@@ -272,15 +283,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
 #pragma unroll
                 for (int st = 0; st < C::nst; ++st) {                 // (nst is even: buffer st & 1, used twice a round)
                     if (it + st >= steps) break;
-                    ok = (it + st < 2 || wait_bar_near(b_tempty + 8 * (st & 1), ((st >> 1) & 1) ^ 1, abort_flag, p.status)) &&
-                         wait_bar_near(b_full + 8 * st, par, abort_flag, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
+                    ok = wait_bar_near(b_full + 8 * st, par, abort_flag, p.status);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tc_mma_f8_pair(tmem + (st & 1) * kPairN, ax0 + st * (C::stage >> 4) + 2 * q,
-                                       ay0 + st * (C::stage >> 4) + 2 * q, idesc, q);
-                    tc_commit_pair(b_tfull + 8 * (st & 1));
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && (it + st < 2 || wait_bar_near(b_tempty + 16 * h + 8 * (st & 1), ((st >> 1) & 1) ^ 1,
+                                                                 abort_flag, p.status));
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc_mma_f8_pair(tmem + (h * 2 + (st & 1)) * (kPairN / 2), ax0 + st * (C::stage >> 4) + 2 * q,
+                                           ay0 + st * (C::stage >> 4) + h * (8192 >> 4) + 2 * q, idesc, q);
+                        tc_commit_pair(b_tfull + 16 * h + 8 * (st & 1));
+                    }
+                    if (!ok) break;
                     tc_commit_pair(b_empty + 8 * st);
                 }
             }
