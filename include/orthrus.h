@@ -473,7 +473,7 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
  *   x         [T, H] of dtype, rows x_stride elements apart.
  *   residual  optional [T, H], dense.  sum_out [T, H], dense, receives s; it is
  *             required with a residual and must be NULL without one.  It may
- *             be the residual itself, or x where x is dense.
+ *             be the residual itself, or x where x is dense, but not out.
  *   weight    [H] of dtype.
  *   out       optional [T, H] of dtype, dense: y.  May be x where x is dense.
  *   out_fp8   optional [T, H] e4m3, dense, with out_scale [T, ceil(H / 128)]
@@ -514,7 +514,7 @@ ORTHRUS_API int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t
  *            (one scale per 128 x 128 block; short blocks at the ends).
  *   out      [M, N] of out_dtype, dense.
  *   status   optional device int32 (ORTHRUS_STATUS_TIMEOUT only).
- * Supported: any M and N, K a multiple of 16; a and w 16-byte aligned (their
+ * Supported: M and N up to 2^30, K a multiple of 16; a and w 16-byte aligned (their
  * rows are then too), out aligned to its element; sm_100 devices only.  No
  * workspace: results do not depend on scheduling and calls may overlap.
  */

@@ -501,7 +501,7 @@ def orthrus_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     pp, pt = _dense(positions, torch.int32, (T,), dev), _dense(turns, torch.float64, None, dev)
     pqn, pkn = _dense(q_norm, dt, (D,), dev), _dense(k_norm, dt, (D,), dev)
     _launch("orthrus_rope", lib().orthrus_rope, dev, _code(dt), layout, pq, pqo, pk, pko, st, pp, pt, magnitude, T, Hq,
-            Hkv, D, 2 * turns.shape[0], pqn, pkn, eps, _on(stream, dev))
+            Hkv, D, 2 * turns.numel(), pqn, pkn, eps, _on(stream, dev))
 
 
 def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -543,7 +543,7 @@ def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v:
     pb, pc = _dense(block_table, torch.int32, None, dev), _dense(ctx_lens, torch.int32, (B,), dev)
     pqn, pkn = _dense(q_norm, dt, (D,), dev), _dense(k_norm, dt, (D,), dev)
     _launch("orthrus_rope_append", lib().orthrus_rope_append, dev, _code(dt), layout, pq, pqo, pk, pv, st, pt, magnitude,
-            B, K, Hq, Hkv, D, 2 * turns.shape[0], pqn, pkn, eps, pkp, pvp, P, page, pb, max_pages, pc,
+            B, K, Hq, Hkv, D, 2 * turns.numel(), pqn, pkn, eps, pkp, pvp, P, page, pb, max_pages, pc,
             _dense(status, torch.int32, None, dev), _on(stream, dev))
 
 

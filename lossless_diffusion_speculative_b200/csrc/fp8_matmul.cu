@@ -432,7 +432,8 @@ int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaS
     p.tiles_x = (p.M + 255) / 256;
     p.tiles_y = (p.N + kPairN - 1) / kPairN;
     const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
-    if (tiles >= 1ll << 28) return ORTHRUS_ERR_UNSUPPORTED;
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    if (tiles >= 1ll << 30 || (tiles / pairs + 1) * p.nkb >= 1ll << 31) return ORTHRUS_ERR_UNSUPPORTED;   // (32-bit steps)
     p.vec = ((uintptr_t)p.out & 15u) == 0 && (int64_t)p.N * (int)sizeof(T) % 16 == 0 &&
             (int64_t)p.N * (int)sizeof(T) < 1ll << 31;
     PairMaps mp;
@@ -447,7 +448,6 @@ int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaS
         mp.o = mp.x;                                                  // (not used)
     }
     if (!pair_ready<T>(dev)) return ORTHRUS_ERR_LAUNCH;
-    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(kPairThreads);
@@ -485,7 +485,7 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     if (!a || !a_scale || !w || !w_scale || !out || M <= 0 || N <= 0 || K <= 0) return ORTHRUS_ERR_ARG;
     const int e = elem_size(out_dtype);
     if (!e) return ORTHRUS_ERR_ARG;
-    if (K % 16) return ORTHRUS_ERR_UNSUPPORTED;
+    if (K % 16 || M > 1 << 30 || N > 1 << 30) return ORTHRUS_ERR_UNSUPPORTED;
     if (((uintptr_t)a | (uintptr_t)w) & 15u) return ORTHRUS_ERR_ALIGN;
     if (((uintptr_t)out & (uintptr_t)(e - 1)) || (((uintptr_t)a_scale | (uintptr_t)w_scale) & 3u)) return ORTHRUS_ERR_ALIGN;
     int dev = 0, sms = 0, major = 0;

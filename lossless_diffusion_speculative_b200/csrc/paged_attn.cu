@@ -189,11 +189,13 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     pdl_wait();
 
     // ---- the flat tile order: exclusive prefix of the sequences' tile counts
+    for (int b = threadIdx.x; b < p.B; b += kThreads) pre[b] = (visible(p, b, blockIdx.x == 0) + kTile - 1) / kTile;
+    __syncthreads();
     if (warp == 0) {
         int run = 0, n_max = 0, n_min = 0x7fffffff, held = 0;     // tiles per segment, sequences with any
         for (int b0 = 0; b0 < p.B; b0 += 32) {
             const int b = b0 + lane;
-            int n = b < p.B ? (visible(p, b, blockIdx.x == 0) + kTile - 1) / kTile : 0;
+            const int n = b < p.B ? pre[b] : 0;
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

@@ -359,7 +359,7 @@ extern "C" int orthrus_rmsnorm(orthrus_dtype dtype, const void *x, int64_t x_str
     if (!x || !weight || !elem_size(dtype) || T <= 0 || H <= 0 || !(eps >= 0.f) || isinf(eps)) return ORTHRUS_ERR_ARG;
     if ((residual == nullptr) != (sum_out == nullptr) || (out_fp8 == nullptr) != (out_scale == nullptr))
         return ORTHRUS_ERR_ARG;
-    if ((!out && !out_fp8) || x_stride < (T > 1 ? H : 0)) return ORTHRUS_ERR_ARG;
+    if ((!out && !out_fp8) || (out && out == sum_out) || x_stride < (T > 1 ? H : 0)) return ORTHRUS_ERR_ARG;
     if (H > ORTHRUS_MAX_NORM_WIDTH) return ORTHRUS_ERR_UNSUPPORTED;
     if ((int64_t)T * 32 >= (1ll << 31)) return ORTHRUS_ERR_UNSUPPORTED;                  // (units of work are 32-bit)
     // rows of x that are not dense must not be written through another stride

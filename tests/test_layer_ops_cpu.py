@@ -42,6 +42,7 @@ def test_rmsnorm_refusals(lib):
     assert rc(dtype=7) == rc(T=0) == rc(T=-1) == rc(H=0) == ob.ERR_ARG
     assert rc(eps=-1.0) == rc(eps=math.inf) == rc(eps=math.nan) == ob.ERR_ARG
     assert rc(res=P) == rc(sum=P) == ob.ERR_ARG                 # residual and sum_out go together
+    assert rc(res=vp(8192), sum=P, out=P) == ob.ERR_ARG         # two outputs in one place
     assert rc(q=P) == rc(qs=P) == ob.ERR_ARG                    # values and scales go together
     assert rc(xs=63) == ob.ERR_ARG                              # rows overlap
     assert rc(xs=128, out=P, x=P) == ob.ERR_ARG                 # in place through another stride
@@ -76,6 +77,7 @@ def test_fp8_matmul_refusals(lib):
         assert f(P, P, P, P, M, N, K, BF, P, None, None) == ob.ERR_ARG
     assert f(P, P, P, P, 4, 64, 64, 5, P, None, None) == ob.ERR_ARG
     assert f(P, P, P, P, 4, 64, 72, BF, P, None, None) == ob.ERR_UNSUPPORTED
+    assert f(P, P, P, P, (1 << 30) + 1, 64, 64, BF, P, None, None) == ob.ERR_UNSUPPORTED
     assert f(vp(4104), P, P, P, 4, 64, 64, BF, P, None, None) == ob.ERR_ALIGN
     assert f(P, P, vp(4104), P, 4, 64, 64, BF, P, None, None) == ob.ERR_ALIGN
     assert f(P, vp(4098), P, P, 4, 64, 64, BF, P, None, None) == ob.ERR_ALIGN
