@@ -47,7 +47,7 @@ struct Args {
     int tiles_x, tiles_y;                // tiles of the weight (pair: token) rows, of the others
     int ranges;                          // split == 1: blocks that share the weight rows of one token tile
     int out_dtype;
-    int vec;                             // every fourth column of out (pair: every row) is aligned
+    int vec;                             // columns of out that one aligned store takes: 4, 2 or 1 (pairs of CTAs: 16 bytes' worth)
 };
 
 constexpr int kXBytes = 128 * 128;
@@ -65,10 +65,19 @@ template <int NT, int GRP, int NST> struct Conf {
     static_assert(total <= 227 * 1024, "shared memory");
 };
 
-// Four consecutive columns of one row, the first n of them inside the matrix.
-template <typename T> __device__ __forceinline__ void put4(T *out, float4 x, int n, bool vec)
+// Four consecutive columns of one row, the first n of them inside the matrix,
+// stored `vec` (4, 2, 1) at a time.
+template <typename T> __device__ __forceinline__ void put2(T *out, float a, float b)
 {
-    if (vec && n >= 4) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t *>(out) = pack2<T>(a, b);
+    else *reinterpret_cast<float2 *>(out) = make_float2(a, b);
+}
+template <typename T> __device__ __forceinline__ void put4(T *out, float4 x, int n, int vec)
+{
+    if (vec == 2 && n >= 2) {                  // (n is even where the rows are)
+        put2(out, x.x, x.y);
+        if (n >= 4) put2(out + 2, x.z, x.w);
+    } else if (vec == 4 && n >= 4) {
         if constexpr (sizeof(T) == 2)
             *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(x.x, x.y), pack2<T>(x.z, x.w));
         else
@@ -374,7 +383,10 @@ int launch_rows(Args &p, const void *a, const void *w, int dev, int sms, cudaStr
     using C = Conf<NT, GRP, NST>;
     p.tiles_x = (p.N + 127) / 128;
     p.tiles_y = (p.M + NT - 1) / NT;
-    p.vec = ((uintptr_t)p.out & (uintptr_t)(4 * elem_size(p.out_dtype) - 1)) == 0 && p.N % 4 == 0;
+    const uintptr_t oe = (uintptr_t)elem_size(p.out_dtype);
+    p.vec = ((uintptr_t)p.out & (4 * oe - 1)) == 0 && p.N % 4 == 0   ? 4
+            : ((uintptr_t)p.out & (2 * oe - 1)) == 0 && p.N % 2 == 0 ? 2
+                                                                     : 1;
     const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
     // fewer tiles than half the SMs: split K over a cluster; else 16-row granules over the SMs
     int split = (int)(tiles * 2 <= sms ? sms / tiles : 1);
@@ -434,15 +446,18 @@ int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaS
     const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
     const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
     if (tiles >= 1ll << 30 || (tiles / pairs + 1) * p.nkb >= 1ll << 31) return ORTHRUS_ERR_UNSUPPORTED;   // (32-bit steps)
-    p.vec = ((uintptr_t)p.out & 15u) == 0 && (int64_t)p.N * (int)sizeof(T) % 16 == 0 &&
-            (int64_t)p.N * (int)sizeof(T) < 1ll << 31;
+    const uintptr_t oa = (uintptr_t)p.out;
+    const int64_t row = (int64_t)p.N * (int)sizeof(T);
+    p.vec = (oa & 15u) == 0 && row % 16 == 0 && row < 1ll << 31 ? 16 / (int)sizeof(T)
+            : (oa & (2 * sizeof(T) - 1)) == 0 && p.N % 2 == 0   ? 2
+                                                                : 1;
     PairMaps mp;
     const uint64_t str[1] = {(uint64_t)p.K}, ostr[1] = {(uint64_t)p.N * sizeof(T)};
     const uint64_t dx[2] = {(uint64_t)p.K, (uint64_t)p.M}, dy[2] = {(uint64_t)p.K, (uint64_t)p.N},
                    dz[2] = {(uint64_t)p.N * sizeof(T), (uint64_t)p.M};
     const uint32_t bx[2] = {128, 128}, by[2] = {128, 64};
     if (!encode_u8_sw128(&mp.x, 2, a, dx, str, bx) || !encode_u8_sw128(&mp.y, 2, w, dy, str, by)) return ORTHRUS_ERR_LAUNCH;
-    if (p.vec) {
+    if (p.vec > 2) {
         if (!encode_u8_sw128(&mp.o, 2, p.out, dz, ostr, bx)) return ORTHRUS_ERR_LAUNCH;
     } else {
         mp.o = mp.x;                                                  // (not used)

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                 }
                 fence_proxy_async();
                 half_sync(half);
-                if (p.vec) {
+                if (p.vec > 2) {
                     if ((threadIdx.x & 127) == 0) {
 #pragma unroll
                         for (int b = 0; b < PASS / BOX; ++b)
@@ -225,15 +225,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                                 tma_store_2d(&mp.o, stage_out + b * 16384, (n0 + c0 + b * BOX) * (int)sizeof(T), m0);
                         bulk_commit();
                     }
-                } else {                                              // rows of out not 16-byte aligned: by element
-                    const T *src = reinterpret_cast<const T *>(sm + C::out + half * C::out_half);
-#pragma unroll 1
-                    for (int i = threadIdx.x & 127; i < 128 * PASS; i += 128) {
-                        const int r = i / PASS, c = i % PASS, e = c % BOX;
-                        const int at = (c / BOX) * 16384 + r * 128 + (((e * (int)sizeof(T)) >> 4 ^ (r & 7)) << 4) +
-                                       ((e * (int)sizeof(T)) & 15);
-                        if (m0 + r < p.M && n0 + c0 + c < p.N)
-                            static_cast<T *>(p.out)[(size_t)(m0 + r) * p.N + n0 + c0 + c] = src[at / (int)sizeof(T)];
+                } else {                                              // rows of out not 16-byte aligned: by pairs or elements
+                    const uint8_t *src = sm + C::out + half * C::out_half;
+                    const int V = p.vec;
+#pragma unroll 4
+                    for (int i = threadIdx.x & 127; i < 128 * PASS / V; i += 128) {
+                        const int r = i * V / PASS, c = i * V % PASS, e = c % BOX * (int)sizeof(T);
+                        const uint8_t *at = src + (c / BOX) * 16384 + r * 128 + ((e >> 4 ^ (r & 7)) << 4) + (e & 15);
+                        if (m0 + r < p.M && n0 + c0 + c < p.N) {
+                            T *dst = static_cast<T *>(p.out) + (size_t)(m0 + r) * p.N + n0 + c0 + c;
+                            if (V == 2 && sizeof(T) == 2) *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(at);
+                            else if (V == 2) *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(at);
+                            else *dst = *reinterpret_cast<const T *>(at);
+                        }
                     }
                     half_sync(half);
                 }

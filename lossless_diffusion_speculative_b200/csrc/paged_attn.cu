@@ -116,57 +116,110 @@ template <int D> struct Layout {
     static constexpr int kMask = kWarps * kStages * 4;
     static constexpr int kFixed = kRing + kML + kMask;
     // a warp's O of 16 rows takes the place of the strip it has just read
-    static_assert(2 * kStripBytes >= kRows * D * 4, "O fits a stage");
+    static_assert(2 * kStripBytes >= kRows * D * 4 && 2 * kStripBytes >= 2048, "O and a join's sums fit a stage");
 };
 
-// Output of a segment from its n partials, weighted by the rows' joint maxima
-// and 1 / sums in `ml`: Q four-value pieces per thread at a time, 16 loads in
-// flight.  Partial 0 sits in slot0, partial j in slot1 + 2 (j - 1).
-template <typename T, int D, int Q>
-__device__ __forceinline__ void join_pieces(const Args &p, T *dst, int items, int n, size_t slot0, size_t slot1,
-                                            const float2 *ml)
+// A row's joint maximum and 1 / sum over a segment's n partials (0 and 0 where no
+// key was seen; a sum that is not a number stays one), LP lanes per row.
+template <int LP, class S>
+__device__ __forceinline__ void join_statistics(const Args &p, int rows, int n, S slot_of, float2 *seg_ml)
 {
-    for (int i0 = threadIdx.x; i0 < items; i0 += Q * kThreads) {
+    const int r = threadIdx.x / LP;
+    float M = -INFINITY, l = 0.f;
+    if (r < rows) {
+#pragma unroll 8
+        for (int j = threadIdx.x % LP; j < n; j += LP) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) + r) * 2));
+            const float m = fmaxf(M, ml.x);
+            if (m != -INFINITY) l = l * fast_exp2(M - m) + ml.y * fast_exp2(ml.x - m);
+            M = m;
+        }
+    }
+    float A = M;
+#pragma unroll
+    for (int d = LP / 2; d; d >>= 1) A = fmaxf(A, __shfl_xor_sync(~0u, A, d));
+    l = M == -INFINITY ? 0.f : l * fast_exp2(M - A);
+#pragma unroll
+    for (int d = LP / 2; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
+    if (threadIdx.x % LP == 0 && r < rows)
+        seg_ml[r] = make_float2(A == -INFINITY ? 0.f : A, l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l);
+}
+
+// Output of a segment from its n partials: the four warps take every fourth
+// partial, a lane up to 4 four-value pieces of the rows with the loads of four
+// partials in flight (a segment of one sequence can have a partial from every
+// block of the grid), and are added in order through shared memory (`area(w)`:
+// 2 KB of warp w).  All threads of the block.
+template <typename T, int D, class S, class A>
+__device__ __forceinline__ void join_segment(const Args &p, T *dst, int rows, int n, S slot_of, A area, float2 *seg_ml)
+{
+    constexpr int U = 4;                               // partials in flight per warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (rows <= 4) join_statistics<32>(p, rows, n, slot_of, seg_ml);
+    else if (rows <= 8) join_statistics<16>(p, rows, n, slot_of, seg_ml);
+    else join_statistics<8>(p, rows, n, slot_of, seg_ml);
+    __syncthreads();
+    constexpr int Q = 4;
+    const int items = rows * (D / 4);
+    for (int base = 0; base < items; base += 32 * Q) {
         float4 a[Q];
         float E[Q];
+        const float *ml[Q], *po[Q];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int i = i0 + q * kThreads;
+        for (int q = 0; q < Q; ++q) {                  // (past the last piece: the last again, not stored)
+            int i = base + q * 32 + lane;
+            i = i < items ? i : items - 1;
             a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-            E[q] = i < items ? ml[i / (D / 4)].x : 0.f;
+            E[q] = seg_ml[i / (D / 4)].x;
+            ml[q] = p.part_ml + i / (D / 4) * 2;
+            po[q] = p.part_o + (i / (D / 4)) * D + i % (D / 4) * 4;
         }
-#pragma unroll 16 / Q
-        for (int j = 0; j < n; ++j) {
-            const size_t slot = (j ? slot1 + 2 * (j - 1) : slot0) * kRows;
+#pragma unroll 1
+        for (int j = warp; j < n; j += kWarps * U) {
+            float m[U][Q];
+            float4 v[U][Q];
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int i = i0 + q * kThreads;
-                if (i < items) {
-                    const size_t sl = slot + i / (D / 4);
-                    const float f = fast_exp2(__ldcg(p.part_ml + sl * 2) - E[q]);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + sl * D + i % (D / 4) * 4));
-                    a[q].x += v.x * f, a[q].y += v.y * f, a[q].z += v.z * f, a[q].w += v.w * f;
+            for (int u = 0; u < U; ++u) {
+                const int ju = j + u * kWarps;
+                const size_t slot = slot_of(ju < n ? ju : j);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    m[u][q] = __ldcg(ml[q] + slot * 2);
+                    v[u][q] = __ldcg(reinterpret_cast<const float4 *>(po[q] + slot * D));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const float f = j + u * kWarps < n ? fast_exp2(m[u][q] - E[q]) : 0.f;
+                    if (j + u * kWarps < n)
+                        a[q].x += v[u][q].x * f, a[q].y += v[u][q].y * f, a[q].z += v[u][q].z * f, a[q].w += v[u][q].w * f;
                 }
             }
         }
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int i = i0 + q * kThreads;
+        for (int q = 0; q < Q; ++q)
+            if (base + q * 32 + lane < items) area(warp)[q * 32 + lane] = a[q];
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 32 * Q / kThreads; ++q) {
+            const int k = q * kThreads + threadIdx.x, i = base + k;
             if (i < items) {
+                float4 x = area(0)[k];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 v = area(w)[k];
+                    x.x += v.x, x.y += v.y, x.z += v.z, x.w += v.w;
+                }
                 const int r = i / (D / 4), d = i % (D / 4) * 4;
-                const float inv = ml[r].y;
+                const float inv = seg_ml[r].y;
                 *reinterpret_cast<uint2 *>(dst + r * D + d) =
-                    make_uint2(pack2<T>(a[q].x * inv, a[q].y * inv), pack2<T>(a[q].z * inv, a[q].w * inv));
+                    make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
             }
         }
+        __syncthreads();
     }
-}
-template <typename T, int D>
-__device__ __forceinline__ void join_rows(const Args &p, T *dst, int rows, int n, size_t slot0, size_t slot1, const float2 *ml)
-{
-    const int items = rows * (D / 4);
-    if (items <= kThreads) join_pieces<T, D, 1>(p, dst, items, n, slot0, slot1, ml);
-    else join_pieces<T, D, 4>(p, dst, items, n, slot0, slot1, ml);
 }
 
 // (blocks of D = 64 and 128 fit twice into an SM)
@@ -215,15 +268,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
         held = __reduce_add_sync(~0u, held);
         if (lane == 0) {
             pre[p.B] = run;
-            // Blocks with work.  Segments of equal length take whole blocks each,
-            // so that no block straddles two, and one block where a join
-            // (~3.5 us of dependent steps) would cost more than the tiles it
-            // spreads (~1.1 us each, measured on one sequence).
+            // Blocks with work: not so many that a join's partials (~0.05 us each
+            // and 128 pieces of output) outweigh the tiles a block is spared
+            // (~0.9 us each), and for a segment of up to 3 tiles one (a join
+            // takes ~3 us even of two).  Segments of equal length take whole
+            // blocks each, so that none straddles two.
             const int64_t total = (int64_t)run * segs, seg = (int64_t)held * segs;
+            const int rows = p.G < kRows ? p.G : kRows, pieces = (rows * (D / 4) + 127) / 128;
             int64_t P = total < gridDim.x ? total : gridDim.x;
-            if (n_max == n_min && seg <= gridDim.x) {
-                const int64_t k = gridDim.x / seg;
-                P = seg * (n_max <= 3 ? 1 : k < n_max ? k : n_max);
+            if (seg > 0) {
+                const int64_t most = (int64_t)sqrtf(18.f * ((float)total / (float)seg) / (float)pieces) + 1;
+                if (n_max == n_min && seg <= gridDim.x) {
+                    int64_t k = gridDim.x / seg;
+                    k = k < most ? k : most;
+                    P = seg * (n_max <= 3 ? 1 : k < n_max ? k : n_max);
+                } else if (P > seg * most) {
+                    P = seg * most;
+                }
             }
             blocks = (int)P;
         }
@@ -511,30 +572,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                     // every other block's range begins inside it)
                     const size_t slot0 = 2 * (size_t)c_first + (range(c_first) < s0 ? 1 : 0);
                     auto slot_of = [&](int j) { return (j ? 2 * (size_t)(c_first + j) : slot0) * kRows; };
-                    // the rows' maxima and sums: eight lanes per row, over the partials
-                    {
-                        const int r = threadIdx.x >> 3;
-                        float M = -INFINITY, l = 0.f;
-                        if (r < rows) {
-#pragma unroll 4
-                            for (int j = threadIdx.x & 7; j < n; j += 8) {
-                                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + (slot_of(j) + r) * 2));
-                                const float m = fmaxf(M, ml.x);
-                                if (m != -INFINITY) l = l * fast_exp2(M - m) + ml.y * fast_exp2(ml.x - m);
-                                M = m;
-                            }
-                        }
-                        float A = M;
-#pragma unroll
-                        for (int d = 4; d; d >>= 1) A = fmaxf(A, __shfl_xor_sync(~0u, A, d));
-                        l = M == -INFINITY ? 0.f : l * fast_exp2(M - A);
-#pragma unroll
-                        for (int d = 4; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-                        if ((threadIdx.x & 7) == 0)               // (a sum that is not a number stays one)
-                            seg_ml[r] = make_float2(A == -INFINITY ? 0.f : A, l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l);
-                    }
-                    __syncthreads();
-                    join_rows<T, D>(p, dst, rows, n, slot0, 2 * (size_t)(c_first + 1), seg_ml);
+                    join_segment<T, D>(p, dst, rows, n, slot_of,
+                                       [&](int w) { return reinterpret_cast<float4 *>(comb_o(w)); }, seg_ml);
                 }
             }
             __syncthreads();                       // the combine buffer and the flag are free again

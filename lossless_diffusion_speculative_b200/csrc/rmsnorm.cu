@@ -9,8 +9,8 @@
 // belongs to W warps (1..32), each lane holding NC chunks of 8 values; the sum
 // of squares goes through shuffles and, for W > 1, shared memory.  A 128-column
 // group lies within one warp's chunk of 256 columns: 16 lanes of 8 consecutive
-// values on the vector path, or four strips of 32 lanes where rows are not
-// 16-byte aligned (V = 1), so its maximum needs shuffles only.  HBM-bound.
+// values on the vector path, or strips of 32 lanes where rows are not 16-byte
+// aligned, so its maximum needs shuffles only.  HBM-bound.
 #include <math.h>
 
 #include "kernels.h"
@@ -192,8 +192,13 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const NormArgs p)
 }
 
 // ---- element path: rows that are not 16-byte aligned, or whose width is not a
-// multiple of 8.  The same parts of a row, four strips of 32 lanes per group.
-template <typename T, int NC, bool NORM, int MAXT>
+// multiple of 8.  The same parts of a row; a lane's 8 values of a chunk are V at
+// a time, strips of 32 V columns: single values, or pairs where every row is
+// aligned for them.
+template <typename T, int V> struct alignas(sizeof(T) * V) Few {
+    T v[V];
+};
+template <typename T, int V, int NC, bool NORM, int MAXT>
 __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
 {
     __shared__ float part[32];
@@ -208,31 +213,41 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
     sm100::pdl_trigger();
     sm100::pdl_wait();
 
-    // column of value j of chunk c: chunk c of warp wr covers 256 columns
-    auto col = [&](int c, int j) { return (c * W + wr) * 256 + j * 32 + lane; };
-    const T *x = static_cast<const T *>(p.x) + row * p.x_stride;
+    // first column of piece j (V columns) of chunk c: chunk c of warp wr covers 256 columns
+    auto col = [&](int c, int j) { return (c * W + wr) * 256 + (j * 32 + lane) * V; };
+    auto load = [&](const T *src, float (&f)[NC][8]) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8 / V; ++j) {
+                Few<T, V> w = {};
+                if (live && col(c, j) < H) w = *reinterpret_cast<const Few<T, V> *>(src + col(c, j));
+#pragma unroll
+                for (int e = 0; e < V; ++e) f[c][j * V + e] = to_f32<T>(w.v[e]);
+            }
+    };
+    auto store = [&](T *dst, const float (&f)[NC][8]) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8 / V; ++j) {
+                Few<T, V> w;
+#pragma unroll
+                for (int e = 0; e < V; ++e) w.v[e] = from_f32<T>(f[c][j * V + e]);
+                if (live && col(c, j) < H) *reinterpret_cast<Few<T, V> *>(dst + col(c, j)) = w;
+            }
+    };
     float s[NC][8];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[c][j] = live && col(c, j) < H ? to_f32<T>(x[col(c, j)]) : 0.f;
+    load(static_cast<const T *>(p.x) + row * p.x_stride, s);
     if constexpr (NORM) {
         if (p.residual) {
-            const T *r = static_cast<const T *>(p.residual) + row * H;
-            T *so = static_cast<T *>(p.sum_out) + row * H;
             float a[NC][8];
+            load(static_cast<const T *>(p.residual) + row * H, a);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a[c][j] = live && col(c, j) < H ? to_f32<T>(r[col(c, j)]) : 0.f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (live && col(c, j) < H) {
-                        s[c][j] += a[c][j];
-                        so[col(c, j)] = from_f32<T>(s[c][j]);
-                    }
+                for (int j = 0; j < 8; ++j) s[c][j] += a[c][j];
+            store(static_cast<T *>(p.sum_out) + row * H, s);
         }
         float q = 0.f;
 #pragma unroll
@@ -247,20 +262,13 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
             for (int w = 0; w < W; ++w) q += part[warp - wr + w];
         }
         const float inv = 1.0f / sqrtf(q / (float)H + p.eps);
-        const T *wt = static_cast<const T *>(p.weight);
+        float w[NC][8];
+        load(static_cast<const T *>(p.weight), w);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s[c][j] = col(c, j) < H ? s[c][j] * inv * to_f32<T>(wt[col(c, j)]) : 0.f;
-        if (p.out && live) {
-            T *o = static_cast<T *>(p.out) + row * H;
-#pragma unroll
-            for (int c = 0; c < NC; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (col(c, j) < H) o[col(c, j)] = from_f32<T>(s[c][j]);
-        }
+            for (int j = 0; j < 8; ++j) s[c][j] = col(c, j / V) < H ? s[c][j] * inv * w[c][j] : 0.f;
+        if (p.out) store(static_cast<T *>(p.out) + row * H, s);
     }
     if (!NORM || p.out_fp8) {
         uint8_t *o = p.out_fp8 + row * H;
@@ -278,8 +286,12 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
 #pragma unroll
                 for (int j = 4 * h; j < 4 * h + 4; j += 2) {
                     const uint32_t v = quotient2(make_float2(s[c][j], s[c][j + 1]), sc);
-                    if (col(c, j) < H) o[col(c, j)] = (uint8_t)v;
-                    if (col(c, j + 1) < H) o[col(c, j + 1)] = (uint8_t)(v >> 8);
+                    if constexpr (V == 2) {
+                        if (col(c, j / 2) < H) *reinterpret_cast<uint16_t *>(o + col(c, j / 2)) = (uint16_t)v;
+                    } else {
+                        if (col(c, j) < H) o[col(c, j)] = (uint8_t)v;
+                        if (col(c, j + 1) < H) o[col(c, j + 1)] = (uint8_t)(v >> 8);
+                    }
                 }
                 if (lane == 0 && (g0 + h) * 128 < H) os[g0 + h] = sc.s;
             }
@@ -287,15 +299,18 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
     }
 }
 
-template <typename T, int NC, bool NORM> cudaError_t launch_norm(const NormArgs &a, bool vec, int sms, cudaStream_t st)
+template <typename T, int NC, bool NORM> cudaError_t launch_norm(const NormArgs &a, int vec, int sms, cudaStream_t st)
 {
     const int warps = NORM && a.W > 8 ? a.W : 8;
     int64_t blocks = ((int64_t)a.T * a.W + warps - 1) / warps;
-    if (!vec) {
+    if (vec < 8) {
         const dim3 grid((unsigned)blocks);
-        if constexpr (NORM)
-            if (warps > 8) return launch_pdl(norm_any_kernel<T, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
-        return launch_pdl(norm_any_kernel<T, NC, NORM, 256>, grid, warps * 32, 0, st, a);
+        if constexpr (NORM) {
+            if (warps > 8 && vec == 2) return launch_pdl(norm_any_kernel<T, 2, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
+            if (warps > 8) return launch_pdl(norm_any_kernel<T, 1, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
+        }
+        if (vec == 2) return launch_pdl(norm_any_kernel<T, 2, NC, NORM, 256>, grid, warps * 32, 0, st, a);
+        return launch_pdl(norm_any_kernel<T, 1, NC, NORM, 256>, grid, warps * 32, 0, st, a);
     }
     const int64_t resident = (int64_t)sms * (warps > 8 ? 1 : NORM ? 2 : 4);
     const dim3 grid((unsigned)(blocks < resident ? blocks : resident));
@@ -306,13 +321,14 @@ template <typename T, int NC, bool NORM> cudaError_t launch_norm(const NormArgs 
     return launch_pdl(norm_rows_kernel<T, NC, NORM, 256>, grid, warps * 32, 0, st, a);
 }
 
-template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, bool vec, int sms, cudaStream_t st)
+template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, int vec, int sms, cudaStream_t st)
 {
     // Chunks per lane and warps per row: few rows spread a row over as many
     // warps as it has chunks (latency); many rows give a lane up to four chunks
     // (more loads in flight, fewer partial sums).
     const int chunks = (a.H + 255) / 256;
-    int nc = a.T <= 2 * sms ? 1 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+    // (The element path holds no loads back and so gains more from more warps.)
+    int nc = a.T <= 2 * sms || vec < 8 ? 1 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
     while (NORM && nc < 4 && nc * 32 < chunks) nc *= 2;
     a.W = (chunks + nc - 1) / nc;
     if (NORM) {                                  // a block holds whole rows
@@ -334,7 +350,11 @@ template <bool NORM> int norm_call(int dtype, NormArgs &a, void *stream)
         (uintptr_t)(e - 1))
         return ORTHRUS_ERR_ALIGN;
     if ((uintptr_t)a.out_scale & 3u) return ORTHRUS_ERR_ALIGN;
-    const bool vec = (ptrs & 15u) == 0 && a.H % 8 == 0 && a.x_stride % 8 == 0;
+    // values at a time: 8 (a 16-byte load of a 16-bit type), or pairs, or one
+    const uintptr_t pair = 2 * (uintptr_t)e - 1;
+    const int vec = (ptrs & 15u) == 0 && a.H % 8 == 0 && a.x_stride % 8 == 0                      ? 8
+                    : (ptrs & pair) == 0 && a.H % 2 == 0 && a.x_stride % 2 == 0 ? 2
+                                                                                                  : 1;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ORTHRUS_ERR_DEVICE;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
