@@ -14,8 +14,8 @@
 // weights are streamed once; bound by HBM.  The weight rows are cut into ranges
 // of 16-row granules, one per block, walked in tiles of up to 128 rows with the
 // loads running ahead across tiles.  Where whole tiles are too few for the SMs
-// a K split over a cluster of blocks (partials joined through distributed
-// shared memory, in rank order) fills them.  The steps of the pipeline are
+// a range goes to a cluster of blocks that split K (partials joined through
+// distributed shared memory, in rank order).  The steps of the pipeline are
 // groups of GRP k-blocks: every wait, signal and issue of a step costs 50-150
 // cycles of latency, which per single block (530 cycles a block measured, 16 KB
 // of weights) was more than the SM's share of HBM takes to deliver it.
@@ -35,7 +35,7 @@ namespace f8 {
 using namespace sm100;
 
 struct Maps {
-    CUtensorMap w, w16, a;               // weights: box 128 x 128 and 128 x 16 rows; tokens: box 128 x NT
+    CUtensorMap w, w32, w16, a;          // weights: boxes of 128, 32 and 16 rows; tokens: NT rows
 };
 
 struct Args {
@@ -45,7 +45,7 @@ struct Args {
     int M, N, K, nkb;
     int split;                           // blocks of a cluster, along K
     int tiles_x, tiles_y;                // tiles of the weight (pair: token) rows, of the others
-    int ranges;                          // split == 1: blocks that share the weight rows of one token tile
+    int ranges;                          // blocks (clusters) that share the weight rows of one token tile
     int out_dtype;
     int vec;                             // columns of out that one aligned store takes: 4, 2 or 1 (pairs of CTAs: 16 bytes' worth)
 };
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(Conf<NT, GRP, NST>::threads, 1)
     }
     if (warp == 4 && lane == 0) {
         tma_prefetch(&mp.w);
+        tma_prefetch(&mp.w32);
         tma_prefetch(&mp.w16);
         tma_prefetch(&mp.a);
     }
@@ -141,19 +142,10 @@ __global__ void __launch_bounds__(Conf<NT, GRP, NST>::threads, 1)
     const uint32_t tmem = misc[0];
 
     // this block's weight rows [r_lo, r_hi), token rows from y0, k-blocks [k_lo, k_hi)
-    int rank = 0, y0, r_lo, r_hi;
-    if (p.split > 1) {
-        rank = blockIdx.x % p.split;
-        const int t = blockIdx.x / p.split;
-        y0 = t / p.tiles_x * NT;
-        r_lo = t % p.tiles_x * 128;
-        r_hi = r_lo + 128;
-    } else {
-        const int g16 = (p.N + 15) >> 4, c = blockIdx.x % p.ranges;
-        y0 = blockIdx.x / p.ranges * NT;
-        r_lo = 16 * (int)((int64_t)c * g16 / p.ranges);
-        r_hi = 16 * (int)((int64_t)(c + 1) * g16 / p.ranges);
-    }
+    const int rank = blockIdx.x % p.split, unit = blockIdx.x / p.split, range = unit % p.ranges;
+    const int g16 = (p.N + 15) >> 4, y0 = unit / p.ranges * NT;
+    const int r_lo = 16 * (int)((int64_t)range * g16 / p.ranges);
+    int r_hi = 16 * (int)((int64_t)(range + 1) * g16 / p.ranges);
     if (r_hi > p.N) r_hi = p.N;
     const int k_lo = (int)((int64_t)rank * p.nkb / p.split), k_hi = (int)((int64_t)(rank + 1) * p.nkb / p.split);
     const int ng = (k_hi - k_lo + GRP - 1) / GRP;                     // groups of a tile
@@ -271,7 +263,10 @@ __global__ void __launch_bounds__(Conf<NT, GRP, NST>::threads, 1)
                         if (rows == 128) {
                             tma_load_2d_hint(dx + j * kXBytes, &mp.w, full, (k0 + j) * 128, x0, pw);
                         } else {
-                            for (int r = 0; r < rows; r += 16)
+                            int r = 0;
+                            for (; r + 32 <= rows; r += 32)
+                                tma_load_2d_hint(dx + j * kXBytes + r * 128, &mp.w32, full, (k0 + j) * 128, x0 + r, pw);
+                            if (r < rows)
                                 tma_load_2d_hint(dx + j * kXBytes + r * 128, &mp.w16, full, (k0 + j) * 128, x0 + r, pw);
                         }
                     }
@@ -331,7 +326,7 @@ __global__ void __launch_bounds__(Conf<NT, GRP, NST>::threads, 1)
 #pragma unroll 1
             for (int c = rank + warp * p.split; c < NT; c += 6 * p.split) {
                 const int n = r_lo + lane * 4;
-                if (y0 + c >= p.M || n >= p.N) continue;
+                if (y0 + c >= p.M || n >= r_hi) continue;
                 const uint32_t at = base + C::tile + (uint32_t)(c * 128 + lane * 4) * 4u;
                 float4 v[8];
 #pragma unroll
@@ -341,7 +336,7 @@ __global__ void __launch_bounds__(Conf<NT, GRP, NST>::threads, 1)
 #pragma unroll
                 for (int r = 1; r < 8; ++r)
                     if (r < p.split) x.x += v[r].x, x.y += v[r].y, x.z += v[r].z, x.w += v[r].w;
-                put4_any(p, (size_t)(y0 + c) * p.N + n, x, p.N - n);
+                put4_any(p, (size_t)(y0 + c) * p.N + n, x, r_hi - n);
             }
         }
         cluster_sync_relaxed();                                       // no block leaves while its partials are read
@@ -364,21 +359,42 @@ namespace f8 {
 
 constexpr int kMaxDevices = 64;
 
-template <int NT, int GRP, int NST> bool rows_ready(int dev)
+// Per device: the kernel's shared memory allowed, and how many clusters of 1, 2,
+// 4 and 8 of its blocks the device holds at once (clusters do not cross the
+// device's processor groups, so these are fewer than SMs / size).
+template <int NT, int GRP, int NST> const int *rows_ready(int dev)
 {
     static std::once_flag once[kMaxDevices];
-    static bool ok[kMaxDevices];
-    if (dev < 0 || dev >= kMaxDevices) return false;
+    static int held[kMaxDevices][4];
+    if (dev < 0 || dev >= kMaxDevices) return nullptr;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(fp8_rows_kernel<NT, GRP, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Conf<NT, GRP, NST>::total) == cudaSuccess;
-        if (!ok[dev]) cudaGetLastError();
+        using C = Conf<NT, GRP, NST>;
+        bool ok = cudaFuncSetAttribute(fp8_rows_kernel<NT, GRP, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::total) == cudaSuccess;
+        for (int i = 0; i < 4 && ok; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1u << i);
+            cfg.blockDim = dim3(C::threads);
+            cfg.dynamicSmemBytes = C::total;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << i;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            ok = cudaOccupancyMaxActiveClusters(&held[dev][i], fp8_rows_kernel<NT, GRP, NST>, &cfg) == cudaSuccess;
+        }
+        if (!ok) {
+            cudaGetLastError();
+            held[dev][0] = 0;
+        }
     });
-    return ok[dev];
+    return held[dev][0] > 0 ? held[dev] : nullptr;
 }
 
 template <int NT, int GRP, int NST>
-int launch_rows(Args &p, const void *a, const void *w, int dev, int sms, cudaStream_t st)
+int launch_rows(Args &p, const void *a, const void *w, int dev, cudaStream_t st)
 {
     using C = Conf<NT, GRP, NST>;
     p.tiles_x = (p.N + 127) / 128;
@@ -387,25 +403,33 @@ int launch_rows(Args &p, const void *a, const void *w, int dev, int sms, cudaStr
     p.vec = ((uintptr_t)p.out & (4 * oe - 1)) == 0 && p.N % 4 == 0   ? 4
             : ((uintptr_t)p.out & (2 * oe - 1)) == 0 && p.N % 2 == 0 ? 2
                                                                      : 1;
-    const int64_t tiles = (int64_t)p.tiles_x * p.tiles_y;
-    // fewer tiles than half the SMs: split K over a cluster; else 16-row granules over the SMs
-    int split = (int)(tiles * 2 <= sms ? sms / tiles : 1);
-    if (split > 8) split = 8;
-    if (split > p.nkb) split = p.nkb;
-    p.split = split;
+    const int *held = rows_ready<NT, GRP, NST>(dev);
+    if (!held) return ORTHRUS_ERR_LAUNCH;
+    // The largest K split whose clusters, all resident at once, cover the weight
+    // rows with one tile of up to 128 rows each: a second wave of clusters costs
+    // a whole kernel time (32 x 6144 x 4096: 48 clusters of 3, of which 46 fit,
+    // took 13.4 us).
     const int g16 = (p.N + 15) / 16;
-    p.ranges = p.tiles_y >= sms ? 1 : sms / p.tiles_y;
+    int split = 1;
+    p.ranges = p.tiles_y >= held[0] ? 1 : held[0] / p.tiles_y;
+    for (int i = 1; i < 4; ++i) {
+        const int r = held[i] / p.tiles_y;
+        if ((int64_t)r * 8 < g16 || (1 << i) > p.nkb) continue;
+        split = 1 << i;
+        p.ranges = r;
+    }
     if (p.ranges > g16) p.ranges = g16;
-    const int64_t blocks = split > 1 ? tiles * split : (int64_t)p.ranges * p.tiles_y;
+    p.split = split;
+    const int64_t blocks = (int64_t)p.ranges * p.tiles_y * split;
     if (blocks >= 1ll << 31) return ORTHRUS_ERR_UNSUPPORTED;
     Maps mp;
     const uint64_t str[1] = {(uint64_t)p.K};
     const uint64_t dw[2] = {(uint64_t)p.K, (uint64_t)p.N}, da[2] = {(uint64_t)p.K, (uint64_t)p.M};
-    const uint32_t bw[2] = {128, 128}, b16[2] = {128, 16}, ba[2] = {128, NT};
-    if (!encode_u8_sw128(&mp.w, 2, w, dw, str, bw) || !encode_u8_sw128(&mp.w16, 2, w, dw, str, b16) ||
+    const uint32_t bw[2] = {128, 128}, b32[2] = {128, 32}, b16[2] = {128, 16}, ba[2] = {128, NT};
+    if (!encode_u8_sw128(&mp.w, 2, w, dw, str, bw) || !encode_u8_sw128(&mp.w32, 2, w, dw, str, b32) ||
+        !encode_u8_sw128(&mp.w16, 2, w, dw, str, b16) ||
         !encode_u8_sw128(&mp.a, 2, a, da, str, ba))
         return ORTHRUS_ERR_LAUNCH;
-    if (!rows_ready<NT, GRP, NST>(dev)) return ORTHRUS_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(C::threads);
@@ -519,13 +543,13 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     p.nkb = (K + ORTHRUS_FP8_BLOCK - 1) / ORTHRUS_FP8_BLOCK;
     p.out_dtype = out_dtype;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M <= 16) return f8::launch_rows<16, 4, 3>(p, a, w, dev, sms, st);
-    if (M <= 32) return f8::launch_rows<32, 4, 2>(p, a, w, dev, sms, st);
-    if (M <= 64) return f8::launch_rows<64, 2, 3>(p, a, w, dev, sms, st);
+    if (M <= 16) return f8::launch_rows<16, 4, 3>(p, a, w, dev, st);
+    if (M <= 32) return f8::launch_rows<32, 4, 2>(p, a, w, dev, st);
+    if (M <= 64) return f8::launch_rows<64, 2, 3>(p, a, w, dev, st);
     // Pairs from 129 rows on, unless their 256 x 256 tiles (no K split) leave most
     // SMs idle: 256 x 4096 x 12288 (16 tiles) takes 30 us by rows and 54 by pairs,
     // 256 x 6144 x 4096 (24) 22 and 22, 512 x 6144 x 4096 (48) 40 and 23.
     const int64_t pair_tiles = (int64_t)((M + 255) / 256) * ((N + f8::kPairN - 1) / f8::kPairN);
-    if (M <= 128 || pair_tiles * 6 <= sms) return f8::launch_rows<128, 2, 2>(p, a, w, dev, sms, st);
+    if (M <= 128 || pair_tiles * 6 <= sms) return f8::launch_rows<128, 2, 2>(p, a, w, dev, st);
     return f8::launch_pair(p, a, w, dev, sms, st);
 }
