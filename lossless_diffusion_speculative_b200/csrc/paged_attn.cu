@@ -5,15 +5,18 @@
 //
 // What bounds it: each key and value is used by the G = Hq / Hkv query heads of
 // its KV head only, 2 G flop per byte, so the keys and values are streamed once
-// from HBM and everything else has to hide behind that stream.  G <= 16 rows
-// would fill an eighth of a tcgen05 tile's 128 and pay its TMEM round trips per
-// tile, so the products run on mma.sync m16n8k16 with the heads as the 16 rows:
-// 48 such instructions per 16 keys x 128 dims (8 KB) against the ~350 cycles
-// the SM's share of HBM needs to deliver them.
+// from HBM and everything else has to hide behind that stream, within the
+// board's power: under a sustained load that reaches the power limit the clocks,
+// and the memory rate with them, fall (by 11 % for twice the matrix
+// instructions).  G <= 16 rows would fill an eighth of a tcgen05 tile's 128 and
+// pay its TMEM round trips per tile, so the products run on mma.sync m16n8k16,
+// transposed: 16 keys (then 16 dims) are the instruction's rows and 8 heads its
+// columns, so that up to 8 heads waste nothing.  The weights go from the first
+// product's layout to the second's by 8 x 8 transposes in registers.
 //
-// Work split: every sequence's keys are cut into tiles of 64 (128 for D = 64); the tiles of all
-// (sequence, KV head, group of 16 heads) segments are laid end to end and cut
-// into equal contiguous ranges, one per block, computed on the device from
+// Work split: every sequence's keys are cut into tiles of 64 (128 for D = 64);
+// the tiles of all (sequence, KV head, group of 16 heads) segments are laid end
+// to end and cut into equal contiguous ranges, one per block, computed on the device from
 // ctx_lens.  Each of the block's four warps takes a quarter of a tile and runs its
 // own cp.async ring and its own running maximum and sum (no block-wide barrier
 // inside a segment); the four are combined through shared memory when the block
@@ -40,7 +43,7 @@ using namespace sm100;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;                        // query heads per segment (the MMA's M)
+constexpr int kRows = 16;                        // query heads per segment, at most
 constexpr int kMaxB = 4096;
 constexpr float kLazy = 8.f;                     // log2 units
 
@@ -81,6 +84,14 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(a)
                  : "memory");
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values spread over the warp (row lane / 4).
+__device__ __forceinline__ uint32_t transpose8(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
 }
 
 template <typename T>
@@ -223,7 +234,8 @@ __device__ __forceinline__ void join_segment(const Args &p, T *dst, int rows, in
 }
 
 // (blocks of D = 64 and 128 fit twice into an SM)
-template <typename T, int D>
+// NH: groups of 8 heads per segment (1 or 2).
+template <typename T, int D, int NH>
 __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(const Args p)
 {
     using L = Layout<D>;
@@ -379,28 +391,35 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
         cp_commit();
     }
 
-    // ---- per-segment state
-    uint32_t qf[D / 16][4];
-    float o[D / 8][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // ---- per-segment state.  This thread's heads in group h: 8 h + 2 (lane & 3)
+    // + {0, 1}; its dims 16 d + lane / 4 + {0, 8}.
+    uint32_t qf[D / 16][NH][2];
+    float o[D / 16][NH][4], m[NH][2], l[NH][2];
     auto load_q = [&]() {
         const int g = cur.g / p.HG, h0 = (cur.g - g * p.HG) * kRows;
-        const int r0 = h0 + (lane >> 2), r1 = r0 + 8;
         const T *q = static_cast<const T *>(p.q) + ((size_t)cur.b * p.Hq + g * p.G) * D + (lane & 3) * 2;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            qf[k][0] = r0 < p.G ? *reinterpret_cast<const uint32_t *>(q + r0 * D + k * 16) : 0u;
-            qf[k][1] = r1 < p.G ? *reinterpret_cast<const uint32_t *>(q + r1 * D + k * 16) : 0u;
-            qf[k][2] = r0 < p.G ? *reinterpret_cast<const uint32_t *>(q + r0 * D + k * 16 + 8) : 0u;
-            qf[k][3] = r1 < p.G ? *reinterpret_cast<const uint32_t *>(q + r1 * D + k * 16 + 8) : 0u;
+        for (int h = 0; h < NH; ++h) {
+            const int r = h0 + h * 8 + (lane >> 2);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qf[k][h][0] = r < p.G ? *reinterpret_cast<const uint32_t *>(q + r * D + k * 16) : 0u;
+                qf[k][h][1] = r < p.G ? *reinterpret_cast<const uint32_t *>(q + r * D + k * 16 + 8) : 0u;
+            }
         }
     };
     auto clear = [&]() {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[d][h][j] = 0.f;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            m[h][0] = m[h][1] = -INFINITY;
+            l[h][0] = l[h][1] = 0.f;
+        }
     };
     load_q();
     clear();
@@ -412,84 +431,112 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
         const uint32_t mask = masks[warp * kStages + stage];
         const uint32_t sk = ring + stage * 2 * L::kStripBytes, sv = sk + L::kStripBytes;
         if (mask) {
-            float s[2 * NS][4];
+            // scores: rows are keys (lane / 4 and + 8 of each 16), columns heads.  Where
+            // there is one accumulator per k, two take turns (the chain of dependent
+            // instructions is half as long).
+            constexpr int CN = NS * NH == 1 ? 2 : 1;
+            float s[NS][NH][4], s2[4];
 #pragma unroll
-            for (int i = 0; i < 2 * NS; ++i)
+            for (int j = 0; j < 4; ++j) s2[j] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int i = 0; i < NS; ++i)
+#pragma unroll
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][h][j] = 0.f;
             {
-                // matrices: keys 0-7 | dims lo, hi, then keys 8-15 | dims lo, hi
-                const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
+                // matrices: dims lo | keys 0-7, 8-15, then dims hi | keys 0-7, 8-15
+                const int r = lane & 15, cc = lane >> 4;
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
-                        uint32_t b[4];
-                        ldsm4(b, sk + (i * 16 + r) * D * 2 + (((2 * k + cc) ^ (r & 7)) << 4));
-                        mma<T>(s[2 * i], qf[k], b[0], b[1]);
-                        mma<T>(s[2 * i + 1], qf[k], b[2], b[3]);
+                        uint32_t a[4];
+                        ldsm4(a, sk + (i * 16 + r) * D * 2 + (((2 * k + cc) ^ (r & 7)) << 4));
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) mma<T>(CN == 2 && (k & 1) ? s2 : s[i][h], a, qf[k][h][0], qf[k][h][1]);
                     }
                 }
             }
-            // columns of this thread: keys 2 (lane & 3) + {0, 1} of each 8
-            const uint32_t mk = mask >> ((lane & 3) * 2);
-            float a0 = -INFINITY, a1 = -INFINITY;
+            if (CN == 2) {
 #pragma unroll
-            for (int i = 0; i < 2 * NS; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s[i][j] = (mk >> (8 * i + (j & 1))) & 1u ? s[i][j] * p.scale_log2 : -INFINITY;
-                a0 = fmax3(a0, s[i][0], s[i][1]);
-                a1 = fmax3(a1, s[i][2], s[i][3]);
+                for (int j = 0; j < 4; ++j) s[0][0][j] += s2[j];
             }
+            if (mask != (kStrip == 32 ? ~0u : 0xffffu)) {
+                const uint32_t mk = mask >> (lane >> 2);
 #pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-                a0 = fmaxf(a0, __shfl_xor_sync(~0u, a0, d));
-                a1 = fmaxf(a1, __shfl_xor_sync(~0u, a1, d));
+                for (int i = 0; i < NS; ++i)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (!((mk >> (16 * i + 8 * (j >> 1))) & 1u)) s[i][h][j] = -INFINITY;
             }
-            if (__any_sync(~0u, a0 > m0 + kLazy || a1 > m1 + kLazy)) {
-                const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-                const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+            float a[NH][2];
+            bool grow = false;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][0] *= f0;
-                    o[i][1] *= f0;
-                    o[i][2] *= f1;
-                    o[i][3] *= f1;
-                }
-                l0 *= f0;
-                l1 *= f1;
-                m0 = n0;
-                m1 = n1;
-            }
-            // a row whose scores so far are all -inf keeps the weights at zero
-            const float e0 = m0 == -INFINITY ? 0.f : m0, e1 = m1 == -INFINITY ? 0.f : m1;
-            uint32_t hi_[NS][4], lo_[NS][4];
+            for (int h = 0; h < NH; ++h) {
 #pragma unroll
-            for (int i = 0; i < 2 * NS; ++i) {
+                for (int e = 0; e < 2; ++e) {
+                    float v = -INFINITY;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float e = h ? e1 : e0;
-                    const float x0 = fast_exp2(s[i][2 * h] - e), x1 = fast_exp2(s[i][2 * h + 1] - e);
-                    if (h) l1 += x0 + x1; else l0 += x0 + x1;
-                    const uint32_t w = pack2<T>(x0, x1);
-                    const float2 back = unpack2<T>(w);
-                    hi_[i / 2][2 * (i & 1) + h] = w;
-                    lo_[i / 2][2 * (i & 1) + h] = pack2<T>(x0 - back.x, x1 - back.y);
+                    for (int i = 0; i < NS; ++i) v = fmax3(v, s[i][h][e], s[i][h][2 + e]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, d));
+                    a[h][e] = v * p.scale_log2;
+                    grow |= a[h][e] > m[h][e] + kLazy;
                 }
             }
-            // matrices: dims lo | keys 0-7, 8-15, then dims hi | keys 0-7, 8-15
-            const int r = lane & 15, cc = lane >> 4;
+            if (__any_sync(~0u, grow)) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float n = fmaxf(m[h][e], a[h][e]);
+                        const float f = m[h][e] == -INFINITY ? 0.f : fast_exp2(m[h][e] - n);
+                        m[h][e] = n;
+                        l[h][e] *= f;
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            o[d][h][e] *= f;
+                            o[d][h][2 + e] *= f;
+                        }
+                    }
+                }
+            }
+            uint32_t hi_[NS][NH][2], lo_[NS][NH][2];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                // a head whose scores so far are all -inf keeps the weights at zero
+                const float e0 = m[h][0] == -INFINITY ? 0.f : m[h][0], e1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {                     // keys lane / 4, + 8
+                        const float x0 = fast_exp2(fmaf(s[i][h][2 * k], p.scale_log2, -e0));
+                        const float x1 = fast_exp2(fmaf(s[i][h][2 * k + 1], p.scale_log2, -e1));
+                        l[h][0] += x0;
+                        l[h][1] += x1;
+                        const uint32_t w = pack2<T>(x0, x1);
+                        const float2 back = unpack2<T>(w);
+                        hi_[i][h][k] = transpose8(w);
+                        lo_[i][h][k] = transpose8(pack2<T>(x0 - back.x, x1 - back.y));
+                    }
+                }
+            }
+            // the values' transpose: matrices keys 0-7 | dims lo, hi, then keys 8-15 | dims lo, hi
+            const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    uint32_t b[4];
-                    ldsm4_t(b, sv + (i * 16 + r) * D * 2 + (((2 * d + cc) ^ (r & 7)) << 4));
-                    mma<T>(o[2 * d], hi_[i], b[0], b[1]);
-                    mma<T>(o[2 * d + 1], hi_[i], b[2], b[3]);
-                    mma<T>(o[2 * d], lo_[i], b[0], b[1]);
-                    mma<T>(o[2 * d + 1], lo_[i], b[2], b[3]);
+                    uint32_t v[4];
+                    ldsm4_t(v, sv + (i * 16 + r) * D * 2 + (((2 * d + cc) ^ (r & 7)) << 4));
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        mma<T>(o[d][h], v, hi_[i][h][0], hi_[i][h][1]);
+                        mma<T>(o[d][h], v, lo_[i][h][0], lo_[i][h][1]);
+                    }
                 }
             }
         }
@@ -502,28 +549,29 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                 advance(cur);
                 load_q();                          // (on its way during the rest)
             }
-#pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-                l0 += __shfl_xor_sync(~0u, l0, d);
-                l1 += __shfl_xor_sync(~0u, l1, d);
-            }
             const int rowsG = p.G - (seg_.g % p.HG) * kRows, rows = rowsG < kRows ? rowsG : kRows;
-            const int r0 = lane >> 2, r1 = r0 + 8;
             // the stage just read holds O now (its next load is issued an iteration
             // later); 8-value chunk i of row r sits at i ^ (r & 7)
             auto comb_o = [&](int w) {
                 return reinterpret_cast<float *>(smem + ((w * kStages + stage) * 2) * L::kStripBytes);
             };
-            float *c0 = comb_o(warp) + r0 * D, *c1 = comb_o(warp) + r1 * D;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const int at = (i ^ r0) * 8 + (lane & 3) * 2;
-                if (r0 < rows) *reinterpret_cast<float2 *>(c0 + at) = make_float2(o[i][0], o[i][1]);
-                if (r1 < rows) *reinterpret_cast<float2 *>(c1 + at) = make_float2(o[i][2], o[i][3]);
-            }
-            if ((lane & 3) == 0) {
-                comb_ml[warp * kRows + r0] = make_float2(m0, l0);
-                comb_ml[warp * kRows + r1] = make_float2(m1, l1);
+            for (int h = 0; h < NH; ++h) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[h][e] += __shfl_xor_sync(~0u, l[h][e], d);
+                    const int r = 8 * h + 2 * (lane & 3) + e;
+                    if (lane < 4) comb_ml[warp * kRows + r] = make_float2(m[h][e], l[h][e]);
+                    if (r < rows) {
+                        float *c = comb_o(warp) + r * D + (lane >> 2);
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            c[((2 * d) ^ (r & 7)) * 8] = o[d][h][e];
+                            c[((2 * d + 1) ^ (r & 7)) * 8] = o[d][h][2 + e];
+                        }
+                    }
+                }
             }
             __syncthreads();
             const int64_t s0 = (int64_t)pre[seg_.b] * segs + (int64_t)seg_.g * seg_.n;      // the segment's flat tiles
@@ -608,25 +656,30 @@ inline Plan plan(int B, int Hq, int Hkv, int D, int sms)
 
 constexpr int kMaxDevices = 64;
 
-template <typename T, int D> bool smem_ready()
+template <typename T, int D, int NH> bool smem_ready()
 {
     static std::once_flag once[kMaxDevices];
     static bool ok[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T, D, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Layout<D>::kFixed + (kMaxB + 1) * (int)sizeof(int)) == cudaSuccess;
         if (!ok[dev]) cudaGetLastError();
     });
     return ok[dev];
 }
 
+template <typename T, int D, int NH> cudaError_t launch_h(const Args &a, int grid, cudaStream_t st)
+{
+    if (!smem_ready<T, D, NH>()) return cudaErrorInvalidValue;
+    const size_t smem = Layout<D>::kFixed + ((size_t)a.B + 1) * sizeof(int);
+    return launch_pdl(paged_attn_kernel<T, D, NH>, dim3(grid), kThreads, smem, st, a);
+}
+
 template <typename T, int D> cudaError_t launch(const Args &a, int grid, cudaStream_t st)
 {
-    if (!smem_ready<T, D>()) return cudaErrorInvalidValue;
-    const size_t smem = Layout<D>::kFixed + ((size_t)a.B + 1) * sizeof(int);
-    return launch_pdl(paged_attn_kernel<T, D>, dim3(grid), kThreads, smem, st, a);
+    return a.G <= 8 ? launch_h<T, D, 1>(a, grid, st) : launch_h<T, D, 2>(a, grid, st);
 }
 
 template <typename T> cudaError_t launch_d(const Args &a, int D, int grid, cudaStream_t st)
