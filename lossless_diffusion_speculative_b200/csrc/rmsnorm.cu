@@ -62,6 +62,42 @@ __device__ __forceinline__ Scale scale_of(float amax)
     return o;
 }
 
+// Maxima of NC chunks' values over 16 lanes, as scales: the butterfly folds chunks
+// together as it goes (with four chunks 5 exchanges instead of 16), each lane
+// makes one scale, and every lane then takes all chunks' from the lanes that
+// hold them.
+template <int NC> __device__ __forceinline__ void scales_of(const float (&m)[NC], Scale (&sc)[NC])
+{
+    const int lane = threadIdx.x & 31;
+    float v;
+    if constexpr (NC == 4) {
+        const bool b0 = lane & 1, b1 = lane & 2;         // the lane keeps chunk (lane & 3)
+        const float a = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(~0u, b0 ? m[0] : m[1], 1));
+        const float b = fmaxf(b0 ? m[3] : m[2], __shfl_xor_sync(~0u, b0 ? m[2] : m[3], 1));
+        v = fmaxf(b1 ? b : a, __shfl_xor_sync(~0u, b1 ? a : b, 2));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+    } else if constexpr (NC == 2) {
+        const bool b0 = lane & 1;
+        v = fmaxf(b0 ? m[1] : m[0], __shfl_xor_sync(~0u, b0 ? m[0] : m[1], 1));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+    } else {
+        v = fmaxf(m[0], __shfl_xor_sync(~0u, m[0], 1));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+    }
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+    const Scale own = scale_of(v);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        sc[c] = own;
+        if (NC > 1) {
+            sc[c].s = __shfl_sync(~0u, own.s, (lane & 16) + c);
+            sc[c].inv = __shfl_sync(~0u, own.inv, (lane & 16) + c);
+        }
+    }
+}
+
 // y / scale, rounded once (the remainder step again), as e4m3: two values, low
 // byte first.  With an infinite scale the quotient is y * 0.
 __device__ __forceinline__ uint32_t quotient2(float2 y, const Scale &sc)
@@ -173,18 +209,23 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const NormArgs p)
             }
         }
         if (!NORM || p.out_fp8) {
+            float m[NC];
+            Scale sc[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                m[c] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[c] = sm100::fmax3(m[c], fabsf(s[c][j].x), fabsf(s[c][j].y));
+            }
+            scales_of<NC>(m, sc);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int k = k0 + c * W * 256;
-                float m = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = sm100::fmax3(m, fabsf(s[c][j].x), fabsf(s[c][j].y));
-                const Scale sc = scale_of(lanes_max(m, 8));
-                const uint32_t lo = quotient2(s[c][0], sc) | (quotient2(s[c][1], sc) << 16);
-                const uint32_t hi = quotient2(s[c][2], sc) | (quotient2(s[c][3], sc) << 16);
+                const uint32_t lo = quotient2(s[c][0], sc[c]) | (quotient2(s[c][1], sc[c]) << 16);
+                const uint32_t hi = quotient2(s[c][2], sc[c]) | (quotient2(s[c][3], sc[c]) << 16);
                 if (live && k < H) {
                     *reinterpret_cast<uint2 *>(p.out_fp8 + (int64_t)r * H + k) = make_uint2(lo, hi);
-                    if ((lane & 15) == 0) p.out_scale[(int64_t)r * groups + (k >> 7)] = sc.s;
+                    if ((lane & 15) == 0) p.out_scale[(int64_t)r * groups + (k >> 7)] = sc[c].s;
                 }
             }
         }
@@ -312,7 +353,7 @@ template <typename T, int NC, bool NORM> cudaError_t launch_norm(const NormArgs 
         if (vec == 2) return launch_pdl(norm_any_kernel<T, 2, NC, NORM, 256>, grid, warps * 32, 0, st, a);
         return launch_pdl(norm_any_kernel<T, 1, NC, NORM, 256>, grid, warps * 32, 0, st, a);
     }
-    const int64_t resident = (int64_t)sms * (warps > 8 ? 1 : NORM ? 2 : 4);
+    const int64_t resident = (int64_t)sms * (warps > 8 ? 1 : NORM ? 2 : 5);
     const dim3 grid((unsigned)(blocks < resident ? blocks : resident));
     if constexpr (NORM) {
         if (warps > 16) return launch_pdl(norm_rows_kernel<T, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
@@ -327,8 +368,11 @@ template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, int vec,
     // warps as it has chunks (latency); many rows give a lane up to four chunks
     // (more loads in flight, fewer partial sums).
     const int chunks = (a.H + 255) / 256;
-    // (The element path holds no loads back and so gains more from more warps.)
+    // (The element path holds no loads back and so gains more from more warps, and
+    // without the norm two chunks and five blocks per SM do better than four and
+    // three: 51 against 57 us at 8192 x 12288.)
     int nc = a.T <= 2 * sms || vec < 8 ? 1 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+    if (!NORM && nc > 2) nc = 2;
     while (NORM && nc < 4 && nc * 32 < chunks) nc *= 2;
     a.W = (chunks + nc - 1) / nc;
     if (NORM) {                                  // a block holds whole rows
