@@ -434,7 +434,8 @@ ORTHRUS_API int orthrus_lm_head_consensus(const void *hidden, const void *lm_hea
  *   q_out        [B, K, Hq, D] bf16 out.
  *   k_cache, v_cache  [B, Hkv, S_max, D] bf16, rows [ctx_b, ctx_b + K) written.
  * Model-specific steps between projection and attention that the pages do
- * not describe (per-head RMSNorm of q and k, rotary embedding) are not applied.
+ * not describe (per-head RMSNorm of q and k, rotary embedding) are not applied;
+ * orthrus_rope_append applies them to the block in place.
  *   workspace    >= orthrus_qkv_workspace_size() bytes, 16-byte aligned,
  *                zero-filled once before first use (its per-tile counters must
  *                be zero when a call starts; every completed call leaves them
