@@ -448,13 +448,13 @@ int launch_rows(Args &p, const void *a, const void *w, int dev, cudaStream_t st)
     return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
 }
 
-template <typename T> bool pair_ready(int dev)
+template <typename T, bool TMA> bool pair_ready(int dev)
 {
     static std::once_flag once[kMaxDevices];
     static bool ok[kMaxDevices];
     if (dev < 0 || dev >= kMaxDevices) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(fp8_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        ok[dev] = cudaFuncSetAttribute(fp8_pair_kernel<T, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        PairConf::total) == cudaSuccess;
         if (!ok[dev]) cudaGetLastError();
     });
@@ -486,7 +486,8 @@ int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaS
     } else {
         mp.o = mp.x;                                                  // (not used)
     }
-    if (!pair_ready<T>(dev)) return ORTHRUS_ERR_LAUNCH;
+    const bool tma = p.vec > 2;
+    if (!(tma ? pair_ready<T, true>(dev) : pair_ready<T, false>(dev))) return ORTHRUS_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(kPairThreads);
@@ -501,7 +502,8 @@ int launch_pair_t(Args &p, const void *a, const void *w, int dev, int sms, cudaS
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T>, mp, p);
+    const cudaError_t e = tma ? cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T, true>, mp, p)
+                              : cudaLaunchKernelEx(&cfg, fp8_pair_kernel<T, false>, mp, p);
     return e == cudaSuccess ? ORTHRUS_OK : ORTHRUS_ERR_LAUNCH;
 }
 

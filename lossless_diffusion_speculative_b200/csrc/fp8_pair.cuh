@@ -12,9 +12,9 @@
 //     separately (706k cycles a call at 8192 x 12288 x 4096 with both halves
 //     together, 610k apart; the multiplications alone are 340k).  The issuing
 //     thread shares its scheduler with two epilogue warps, so what it and they
-//     issue counts: the sums use two-element FMAs (one-element ones: 746k) on
-//     chunks of 16 columns (32: 749k), no votes between signals, one issuing
-//     thread (one per half: 770k).
+//     issue counts: the sums use two-element FMAs but for one pair in eight
+//     (all: 610k, half: 685k, none: 746k), chunks of 16 columns (8: 688k, 32:
+//     715k), no votes between signals, one issuing thread (one per half: 770k).
 //   - the row scales lie [row][k-block] in memory, a line per row: a warp of
 //     its own copies 16 k-blocks of all rows at a time, coalesced along k.
 //     (Loaded by the epilogue's lanes, a row each, the same copies took the L1
@@ -72,15 +72,24 @@ __device__ __forceinline__ void half_sync(int half)
 __device__ __forceinline__ bool half_agree(int half, bool ok)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-                 "barrier.cta.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(1 + half), "r"((uint32_t)ok)
-                 : "memory");
+    if (half)
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                     "barrier.cta.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(r)
+                     : "r"((uint32_t)ok)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                     "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(r)
+                     : "r"((uint32_t)ok)
+                     : "memory");
     return r != 0;
 }
 
-template <typename T>
+// TMA: rows of out are aligned for TMA stores.  (A form of its own: the other
+// path's registers made the sums' loop spill, 676k cycles instead of 610k.)
+template <typename T, bool TMA>
 __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_constant__ PairMaps mp, const Args p)
 {
     using C = PairConf;
@@ -114,7 +123,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
     if (warp == kEpiWarps && lane == 0) {
         tma_prefetch(&mp.x);
         tma_prefetch(&mp.y);
-        tma_prefetch(&mp.o);
+        if (TMA) tma_prefetch(&mp.o);
     }
     if (warp == kEpiWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + C::bars +
@@ -164,27 +173,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                 ok &= wait_bar_near(tfull + 8 * buf, (it >> 1) & 1, abort_flag, p.status);
                 __syncwarp();
                 tc_fence_after();
-                // two chunks of 16 columns: one on its way while the other is added
-                uint32_t v[2][16];
-                tmem_ld16(t_row + buf * CPT, v[0]);
 #pragma unroll
                 for (int c = 0; c < CPT; c += 16) {
+                    uint32_t w[16];
+                    tmem_ld16(t_row + buf * CPT + c, w);
                     tmem_wait_ld();
-                    if (c + 16 < CPT) {
-                        tmem_ld16(t_row + buf * CPT + c + 16, v[(c / 16 + 1) & 1]);
-                    } else {                                          // all read: the buffer is free
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive_cluster(lead_tempty + 8 * buf);
-                            if (in == kScaleGroup - 1 || kb + 1 == p.nkb) mbar_arrive(b_sempty + 8 * gb);
-                        }
-                    }
-                    const uint32_t(&w)[16] = v[(c / 16) & 1];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        acc[c / 2 + q] = ffma2(make_float2(__uint_as_float(w[2 * q]), __uint_as_float(w[2 * q + 1])), s2,
-                                               acc[c / 2 + q]);
+                    for (int q = 0; q < 8; ++q) {
+                        // seven pairs in eight by two-element FMAs (half of the FMA pipe,
+                        // half the issue slots), one by the pipe's other half
+                        float2 &x = acc[c / 2 + q];
+                        const float y0 = __uint_as_float(w[2 * q]), y1 = __uint_as_float(w[2 * q + 1]);
+                        if (q == 7) x = make_float2(fmaf(y0, sc, x.x), fmaf(y1, sc, x.y));
+                        else x = ffma2(make_float2(y0, y1), s2, x);
+                    }
+                }
+                // (signalled after the last sums, not after the last load: the MMA
+                // warp's steps are slow while this partition still adds)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_cluster(lead_tempty + 8 * buf);
+                    if (in == kScaleGroup - 1 || kb + 1 == p.nkb) mbar_arrive(b_sempty + 8 * gb);
                 }
             }
             ok = half_agree(half, ok);               // (after an abort all four warps leave together)
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) fp8_pair_kernel(const __grid_
                 }
                 fence_proxy_async();
                 half_sync(half);
-                if (p.vec > 2) {
+                if constexpr (TMA) {
                     if ((threadIdx.x & 127) == 0) {
 #pragma unroll
                         for (int b = 0; b < PASS / BOX; ++b)

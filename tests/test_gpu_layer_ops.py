@@ -655,3 +655,90 @@ def test_layer_captured_replayed_and_on_other_streams():
     torch.cuda.synchronize()
     for l, w in zip(layers, want):
         assert all(torch.equal(a, b) for a, b in zip(l.outputs(), w))
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 2050, 256), (700, 2052, 384), (260, 4095, 128), (40, 1002, 640), (9, 1001, 512),
+                                   (100, 50, 4096), (2, 20, 8192), (513, 1024, 144)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_fp8_matmul_row_alignments_and_splits(M, N, K, out):
+    """Outputs whose rows allow stores of 16 bytes, of pairs or of single values,
+    and shapes whose K is split over a cluster."""
+    g = gen(M + N + K)
+    a, sa, w, sw = fp8_operands(g, M, N, K)
+    for shift in (0, 1, 2):
+        store = torch.full((M * N + 8,), 77.0, dtype=TYPES[out], device="cuda")
+        o = store[shift:shift + M * N].view(M, N)
+        ob.orthrus_fp8_matmul(a, sa, w, sw, o)
+        check_product(o, a, sa, w, sw, f"shift {shift}")
+        assert (store[:shift] == 77).all() and (store[shift + M * N:] == 77).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H", [(4, 70), (600, 1422), (33, 9002), (1, 130)])
+def test_rmsnorm_and_quantize_even_widths(dtype, T, H):
+    """Rows aligned for pairs only."""
+    dt, g = TYPES[dtype], gen(T + H)
+    x, w, r = randn(g, T, H).to(dt), (1 + 0.3 * randn(g, H)).to(dt), randn(g, T, H).to(dt)
+    out, so = torch.empty_like(x), torch.empty_like(x)
+    q, ok = guard(T, H, dtype=torch.float8_e4m3fn)
+    sc = torch.empty(T, (H + 127) // 128, device="cuda")
+    ob.orthrus_rmsnorm(x, w, 1e-5, out=out, residual=r, sum_out=so, out_fp8=q, out_scale=sc)
+    s, y = norm_ref(x, r, w, 1e-5)
+    close(so, s, (half_step(dt) + 2.0 ** -23) * s.abs() + tiny(dt), "sum")
+    close(out, y, (half_step(dt) + 2.0 ** -18) * y.abs() + tiny(dt), "norm")
+    check_fp8(q, sc, y, "norm")
+    ob.orthrus_quantize_fp8(x, q, sc)
+    check_fp8(q, sc, x.double(), "quantize")
+    assert ok()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (5, 1, 128), (12, 1, 64), (16, 1, 256), (9, 1, 128), (24, 1, 64)])
+def test_paged_attn_joins_of_many_blocks(Hq, Hkv, D):
+    """One and two sequences of one KV head, long enough that every block of the
+    grid holds a part, and lengths around a block's share."""
+    g = gen(Hq + D)
+    for lens in ([20000], [30011, 9000], [64, 64, 64], [193, 193]):
+        kp, vp, table = paged_cache(g, lens, 32, Hkv, D, torch.bfloat16)
+        q = randn(g, len(lens), Hq, D).bfloat16()
+        out, st = run_paged(q, kp, vp, table, lens)
+        want, tol = paged_ref(q, kp, vp, table, lens)
+        close(out, want, tol, f"{lens}")
+        assert st == 0
+
+
+def test_paged_attn_on_the_contiguous_cache_matches_the_block_attention():
+    """page_size = S_max, block_table[b] = b: the same keys and values through
+    orthrus_attn with a block of one token (AR view)."""
+    g = gen(77)
+    B, Hq, Hkv, D, S = 3, 32, 8, 128, 520
+    kc, vc = randn(g, B, Hkv, S, D).bfloat16() / 11, randn(g, B, Hkv, S, D).bfloat16() / 11
+    q = randn(g, B, 1, Hq, D).bfloat16()
+    ctx = torch.tensor([500, 0, 77], dtype=torch.int32, device="cuda")
+    ref = torch.empty(B, 1, Hq, D, device="cuda")
+    ws = torch.zeros(ob.orthrus_attn_workspace_size(B, Hq, Hkv, D, 1), dtype=torch.uint8, device="cuda")
+    ob.orthrus_attn(ob.AR, q, kc, vc, ctx, ref, ws)
+    table = torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1)
+    out, st = run_paged(q.view(B, Hq, D), kc, vc, table, [501, 1, 78], n_new=1)
+    # half a step of bf16, and the block attention's own bound (2e-3 of the output's rms)
+    close(out, ref.view(B, Hq, D), 2.0 ** -8 * ref.view(B, Hq, D).double().abs() + 2e-3 * float(ref.pow(2).mean().sqrt()), "views")
+    assert st == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Products of both forms, norms and rotations enqueued on two streams together."""
+    g = gen(88)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    jobs = []
+    for M, N, K in ((600, 1536, 512), (20, 3000, 1024)):
+        a, sa, w, sw = fp8_operands(g, M, N, K)
+        outs = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        ob.orthrus_fp8_matmul(a, sa, w, sw, outs[0])
+        jobs.append((a, sa, w, sw, outs))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for job, st in zip(jobs, sides):
+            a, sa, w, sw, outs = job
+            ob.orthrus_fp8_matmul(a, sa, w, sw, outs[1], stream=st)
+    torch.cuda.synchronize()
+    for *_, outs in jobs:
+        assert torch.equal(outs[0], outs[1])
