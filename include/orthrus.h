@@ -480,8 +480,10 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
  *   out_fp8   optional [T, H] e4m3, dense, with out_scale [T, ceil(H / 128)]
  *             fp32: for each group of 128 columns (the last may be short)
  *                 scale = max(max|y| / 448, 2^-126),  value = e4m3(y / scale)
- *             (nearest even), so value * scale stands for y and a group of
- *             zeros has a finite scale.  A NaN stays a NaN and does not enter
+ *             (nearest; the quotient is y times the fp32 reciprocal of the
+ *             scale, so one that lies on a border between two values can go
+ *             to either), so value * scale stands for y and a group of zeros
+ *             has a finite scale.  A NaN stays a NaN and does not enter
  *             the maximum.
  *             At least one of out and out_fp8 is given.
  * Supported: H <= ORTHRUS_MAX_NORM_WIDTH, any T.  16-byte aligned pointers,

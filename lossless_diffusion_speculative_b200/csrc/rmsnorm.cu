@@ -98,14 +98,14 @@ template <int NC> __device__ __forceinline__ void scales_of(const float (&m)[NC]
     }
 }
 
-// y / scale, rounded once (the remainder step again), as e4m3: two values, low
-// byte first.  With an infinite scale the quotient is y * 0.
+// y / scale as e4m3: two values, low byte first.  The quotient is y times the
+// rounded reciprocal, up to 1.5 units in fp32's last place off: a quotient that
+// lies on a border between two e4m3 values can go to either.  (The remainder
+// step that would round it correctly costs two FMAs a pair, and at the board's
+// power limit 10 % of the time: 58.6 against 52.8 us at 8192 x 12288.)
 __device__ __forceinline__ uint32_t quotient2(float2 y, const Scale &sc)
 {
-    const float2 i = make_float2(sc.inv, sc.inv), ns = make_float2(-sc.s, -sc.s);
-    float2 q = sm100::fmul2(y, i);
-    if (sc.inv != 0.f) q = sm100::ffma2(sm100::ffma2(ns, q, y), i, q);
-    return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    return __nv_cvt_float2_to_fp8x2(sm100::fmul2(y, make_float2(sc.inv, sc.inv)), __NV_SATFINITE, __NV_E4M3);
 }
 
 // ---- vector path
