@@ -334,6 +334,7 @@ def orthrus_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 # (These calls are short on the GPU, so their argument checks are kept to what a
 # few attribute reads per tensor cost.)
 _CODES = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
+_E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -357,11 +358,9 @@ def _fail(t: torch.Tensor, dtype, shape, dev):
     raise ValueError("liborthrus takes contiguous tensors here")
 
 
-def _dense(t: Optional[torch.Tensor], dtype, shape, dev: int):
+def _dense(t: torch.Tensor, dtype, shape, dev: int):
     """Address of a contiguous tensor of this type and shape on device `dev`
-    (None stays None; a None type or shape is not checked)."""
-    if t is None:
-        return None
+    (a None type or shape is not checked)."""
     if ((dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape)
             or t.get_device() != dev or dev < 0 or not t.is_contiguous()):
         _fail(t, dtype, shape, dev)
@@ -375,15 +374,10 @@ def _strided(t: torch.Tensor, dtype, shape, dev: int):
     return t.data_ptr()
 
 
-def _launch(name: str, fn, dev: int, *args) -> None:
-    """Call the entry point with the tensors' device current."""
-    if _current_device() == dev:
-        rc = fn(*args)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args)
-    if rc != 0:
-        _check(name, rc)
+def _elsewhere(dev: int, fn, args) -> int:
+    """The call with the tensors' device current (it is not)."""
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _on(stream, dev: int) -> int:
@@ -394,13 +388,13 @@ def _on(stream, dev: int) -> int:
 
 
 def _rows(x: torch.Tensor):
-    """(T, H, row stride) of a [T, H] tensor whose rows are contiguous."""
-    if x.dim() != 2:
-        raise ValueError(f"expected [rows, width], got {tuple(x.shape)}")
-    T, H = x.shape
-    if H > 1 and x.stride(1) != 1:
+    """(shape, row stride) of a [T, H] tensor whose rows are contiguous."""
+    shape, st = x.shape, x.stride()
+    if len(shape) != 2:
+        raise ValueError(f"expected [rows, width], got {tuple(shape)}")
+    if st[1] != 1 and shape[1] > 1:
         raise ValueError("rows have to be contiguous")
-    return T, H, (x.stride(0) if T > 1 else H)
+    return shape, (st[0] if shape[0] > 1 else shape[1])
 
 
 def orthrus_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Optional[torch.Tensor] = None,
@@ -410,25 +404,32 @@ def orthrus_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Opti
     """x [T,H] (rows may be strided; bf16, fp16 or fp32), weight [H] -> out [T,H]
     and / or out_fp8 [T,H] e4m3 with out_scale [T,ceil(H/128)] fp32; with a
     residual [T,H], x + residual is normed and written to sum_out."""
-    T, H, stride = _rows(x)
-    dt, dev, shape = x.dtype, x.get_device(), x.shape
-    pw = _dense(weight, dt, (H,), dev)
-    po, pr, ps = _dense(out, dt, shape, dev), _dense(residual, dt, shape, dev), _dense(sum_out, dt, shape, dev)
-    pq = _dense(out_fp8, torch.float8_e4m3fn, shape, dev)
-    pc = _dense(out_scale, torch.float32, (T, (H + 127) // 128), dev)
-    _launch("orthrus_rmsnorm", lib().orthrus_rmsnorm, dev, _code(dt), x.data_ptr(), stride, pr, pw, T, H, eps, ps, po,
-            pq, pc, _on(stream, dev))
+    shape, stride = _rows(x)
+    T, H = shape
+    dt, dev = x.dtype, x.get_device()
+    args = (_code(dt), x.data_ptr(), stride, None if residual is None else _dense(residual, dt, shape, dev),
+            _dense(weight, dt, (H,), dev), T, H, eps, None if sum_out is None else _dense(sum_out, dt, shape, dev),
+            None if out is None else _dense(out, dt, shape, dev),
+            None if out_fp8 is None else _dense(out_fp8, _E4M3, shape, dev),
+            None if out_scale is None else _dense(out_scale, _FP32, (T, (H + 127) // 128), dev), _on(stream, dev))
+    fn = (_lib or lib()).orthrus_rmsnorm
+    rc = fn(*args) if _current_device() == dev else _elsewhere(dev, fn, args)
+    if rc:
+        _check("orthrus_rmsnorm", rc)
 
 
 def orthrus_quantize_fp8(x: torch.Tensor, out_fp8: torch.Tensor, out_scale: torch.Tensor, stream=None) -> None:
     """x [T,H] (rows may be strided) -> out_fp8 [T,H] e4m3 and out_scale
     [T,ceil(H/128)] fp32, one scale per row and 128 columns."""
-    T, H, stride = _rows(x)
+    shape, stride = _rows(x)
+    T, H = shape
     dev = x.get_device()
-    pq = _dense(out_fp8, torch.float8_e4m3fn, x.shape, dev)
-    pc = _dense(out_scale, torch.float32, (T, (H + 127) // 128), dev)
-    _launch("orthrus_quantize_fp8", lib().orthrus_quantize_fp8, dev, _code(x.dtype), x.data_ptr(), stride, T, H, pq, pc,
-            _on(stream, dev))
+    args = (_code(x.dtype), x.data_ptr(), stride, T, H, _dense(out_fp8, _E4M3, shape, dev),
+            _dense(out_scale, _FP32, (T, (H + 127) // 128), dev), _on(stream, dev))
+    fn = (_lib or lib()).orthrus_quantize_fp8
+    rc = fn(*args) if _current_device() == dev else _elsewhere(dev, fn, args)
+    if rc:
+        _check("orthrus_quantize_fp8", rc)
 
 
 def orthrus_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -438,12 +439,15 @@ def orthrus_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
     M, K = a.shape
     N = w.shape[0]
     nk = (K + 127) // 128
-    dev, e4m3, f32 = a.get_device(), torch.float8_e4m3fn, torch.float32
-    pa, pw = _dense(a, e4m3, None, dev), _dense(w, e4m3, (N, K), dev)
-    psa, psw = _dense(a_scale, f32, (M, nk), dev), _dense(w_scale, f32, ((N + 127) // 128, nk), dev)
-    po, pst = _dense(out, None, (M, N), dev), _dense(status, torch.int32, None, dev)
-    _launch("orthrus_fp8_matmul", lib().orthrus_fp8_matmul, dev, pa, psa, pw, psw, M, N, K, _code(out.dtype), po, pst,
+    dev = a.get_device()
+    args = (_dense(a, _E4M3, None, dev), _dense(a_scale, _FP32, (M, nk), dev), _dense(w, _E4M3, (N, K), dev),
+            _dense(w_scale, _FP32, ((N + 127) // 128, nk), dev), M, N, K, _code(out.dtype),
+            _dense(out, None, (M, N), dev), None if status is None else _dense(status, torch.int32, None, dev),
             _on(stream, dev))
+    fn = (_lib or lib()).orthrus_fp8_matmul
+    rc = fn(*args) if _current_device() == dev else _elsewhere(dev, fn, args)
+    if rc:
+        _check("orthrus_fp8_matmul", rc)
 
 
 def orthrus_rope_table(rot_dim: int, theta: float, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -498,10 +502,14 @@ def orthrus_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Te
     else:
         Hkv, pk, pko = 0, None, None
         st = _stride_array(*_token_strides(q), *_token_strides(q_out), 0, 0, 0, 0)
-    pp, pt = _dense(positions, torch.int32, (T,), dev), _dense(turns, torch.float64, None, dev)
-    pqn, pkn = _dense(q_norm, dt, (D,), dev), _dense(k_norm, dt, (D,), dev)
-    _launch("orthrus_rope", lib().orthrus_rope, dev, _code(dt), layout, pq, pqo, pk, pko, st, pp, pt, magnitude, T, Hq,
-            Hkv, D, 2 * turns.numel(), pqn, pkn, eps, _on(stream, dev))
+    args = (_code(dt), layout, pq, pqo, pk, pko, st, _dense(positions, torch.int32, (T,), dev),
+            _dense(turns, torch.float64, None, dev), magnitude, T, Hq, Hkv, D, 2 * turns.numel(),
+            None if q_norm is None else _dense(q_norm, dt, (D,), dev),
+            None if k_norm is None else _dense(k_norm, dt, (D,), dev), eps, _on(stream, dev))
+    fn = (_lib or lib()).orthrus_rope
+    rc = fn(*args) if _current_device() == dev else _elsewhere(dev, fn, args)
+    if rc:
+        _check("orthrus_rope", rc)
 
 
 def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
@@ -538,13 +546,16 @@ def orthrus_rope_append(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v:
     else:
         pk, pv = None, None
         st = _stride_array(*st, 0, 0, 0, 0)
-    pt, pkp, pvp = _dense(turns, torch.float64, None, dev), _dense(k_pages, dt, None, dev), _dense(
-        v_pages, dt, k_pages.shape, dev)
-    pb, pc = _dense(block_table, torch.int32, None, dev), _dense(ctx_lens, torch.int32, (B,), dev)
-    pqn, pkn = _dense(q_norm, dt, (D,), dev), _dense(k_norm, dt, (D,), dev)
-    _launch("orthrus_rope_append", lib().orthrus_rope_append, dev, _code(dt), layout, pq, pqo, pk, pv, st, pt, magnitude,
-            B, K, Hq, Hkv, D, 2 * turns.numel(), pqn, pkn, eps, pkp, pvp, P, page, pb, max_pages, pc,
-            _dense(status, torch.int32, None, dev), _on(stream, dev))
+    args = (_code(dt), layout, pq, pqo, pk, pv, st, _dense(turns, torch.float64, None, dev), magnitude, B, K, Hq, Hkv, D,
+            2 * turns.numel(), None if q_norm is None else _dense(q_norm, dt, (D,), dev),
+            None if k_norm is None else _dense(k_norm, dt, (D,), dev), eps, _dense(k_pages, dt, None, dev),
+            None if v_pages is None else _dense(v_pages, dt, k_pages.shape, dev), P, page,
+            _dense(block_table, torch.int32, None, dev), max_pages, _dense(ctx_lens, torch.int32, (B,), dev),
+            None if status is None else _dense(status, torch.int32, None, dev), _on(stream, dev))
+    fn = (_lib or lib()).orthrus_rope_append
+    rc = fn(*args) if _current_device() == dev else _elsewhere(dev, fn, args)
+    if rc:
+        _check("orthrus_rope_append", rc)
 
 
 def orthrus_paged_attn_workspace_size(B: int, Hq: int, Hkv: int, D: int) -> int:
@@ -563,9 +574,11 @@ def orthrus_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Te
     if Dk != D:
         raise ValueError(f"head size {D} of q and {Dk} of the pages")
     dt, dev = q.dtype, q.get_device()
-    pq, po = _dense(q, dt, None, dev), _dense(out, dt, q.shape, dev)
-    pk, pv = _dense(k_pages, dt, None, dev), _dense(v_pages, dt, k_pages.shape, dev)
-    pb, pc = _dense(block_table, torch.int32, (B, max_pages), dev), _dense(ctx_lens, torch.int32, (B,), dev)
-    pw, pst = _dense(workspace, None, None, dev), _dense(status, torch.int32, None, dev)
-    _launch("orthrus_paged_attn", lib().orthrus_paged_attn, dev, _code(dt), pq, pk, pv, pb, pc, n_new, B, Hq, Hkv, D, P,
-            page, max_pages, scale, po, pw, workspace.nbytes, pst, _on(stream, dev))
+    args = (_code(dt), _dense(q, dt, None, dev), _dense(k_pages, dt, None, dev), _dense(v_pages, dt, k_pages.shape, dev),
+            _dense(block_table, torch.int32, (B, max_pages), dev), _dense(ctx_lens, torch.int32, (B,), dev), n_new, B, Hq,
+            Hkv, D, P, page, max_pages, scale, _dense(out, dt, q.shape, dev), _dense(workspace, None, None, dev),
+            workspace.nbytes, None if status is None else _dense(status, torch.int32, None, dev), _on(stream, dev))
+    fn = (_lib or lib()).orthrus_paged_attn
+    rc = fn(*args) if _current_device() == dev else _elsewhere(dev, fn, args)
+    if rc:
+        _check("orthrus_paged_attn", rc)
