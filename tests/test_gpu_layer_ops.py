@@ -673,6 +673,22 @@ def test_fp8_matmul_row_alignments_and_splits(M, N, K, out):
         assert (store[:shift] == 77).all() and (store[shift + M * N:] == 77).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 257, 128), (300, 259, 64), (515, 385, 128), (200, 263, 128), (200, 510, 256),
+                                   (1030, 1291, 64)])
+@pytest.mark.parametrize("out", list(TYPES))
+def test_fp8_matmul_short_runs_at_every_alignment(M, N, K, out):
+    """Last tiles of a few columns, at each of the eight places of a row's start
+    within 16 bytes."""
+    g = gen(M + N + K)
+    a, sa, w, sw = fp8_operands(g, M, N, K)
+    for shift in range(8):
+        store = torch.full((M * N + 8,), 77.0, dtype=TYPES[out], device="cuda")
+        o = store[shift:shift + M * N].view(M, N)
+        ob.orthrus_fp8_matmul(a, sa, w, sw, o)
+        check_product(o, a, sa, w, sw, f"shift {shift}")
+        assert (store[:shift] == 77).all() and (store[shift + M * N:] == 77).all()
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("T,H", [(4, 70), (600, 1422), (33, 9002), (1, 130)])
 def test_rmsnorm_and_quantize_even_widths(dtype, T, H):
