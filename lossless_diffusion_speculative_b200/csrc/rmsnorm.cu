@@ -368,10 +368,12 @@ template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, int vec,
     // warps as it has chunks (latency); many rows give a lane up to four chunks
     // (more loads in flight, fewer partial sums).
     const int chunks = (a.H + 255) / 256;
-    // (The element path holds no loads back and so gains more from more warps, and
-    // without the norm two chunks and five blocks per SM do better than four and
-    // three: 51 against 57 us at 8192 x 12288.)
-    int nc = a.T <= 2 * sms || vec < 8 ? 1 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+    // (The element path holds no loads back and takes as few as keep a row within
+    // eight warps: 92 -> 58 us at 4000 x 4597.  Without the norm two chunks and five
+    // blocks per SM do better than four and three: 51 against 57 us at 8192 x 12288.)
+    int nc = a.T <= 2 * sms ? 1
+             : vec < 8      ? (chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4)
+                            : (chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1);
     if (!NORM && nc > 2) nc = 2;
     while (NORM && nc < 4 && nc * 32 < chunks) nc *= 2;
     a.W = (chunks + nc - 1) / nc;
