@@ -26,7 +26,10 @@
 // Numerics: q.k in fp32 from exact products, running maximum with a lazy
 // rescale (only when a row's maximum grows by more than 2^8), p = 2^(s - m) split
 // into two 16-bit terms p_hi + p_lo for the second product: one 16-bit p would
-// lose 2^-9 (bf16) per weight, the second term is free behind the stream.
+// lose 2^-9 (bf16) per weight, the second term is free behind the stream.  fp16
+// weights are held 2^7 up (2^15 at most): a step of 2^-24 at the bottom of the
+// type's range, against a largest weight of 1, lost up to 1 % of the many small
+// weights of a long cache beside one dominant key.
 #include <math.h>
 
 #include <mutex>
@@ -260,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     constexpr int kStages = L::kStages, kStrip = L::kStrip, kTile = L::kTile;
     constexpr int CH = D / 8;                                        // 16-byte chunks of a row
     constexpr int NS = kStrip / 16;                                  // 16-key steps of a strip
+    constexpr float kUp = std::is_same<T, __half>::value ? 7.f : 0.f;
     extern __shared__ __align__(128) uint8_t smem[];
     float2 *comb_ml = reinterpret_cast<float2 *>(smem + L::kRing);   // [warp][row]
     volatile uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::kRing + L::kML);
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 // a head whose scores so far are all -inf keeps the weights at zero
-                const float e0 = m[h][0] == -INFINITY ? 0.f : m[h][0], e1 = m[h][1] == -INFINITY ? 0.f : m[h][1];
+                const float e0 = m[h][0] == -INFINITY ? 0.f : m[h][0] - kUp, e1 = m[h][1] == -INFINITY ? 0.f : m[h][1] - kUp;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
 #pragma unroll

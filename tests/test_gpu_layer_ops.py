@@ -708,6 +708,29 @@ def test_rmsnorm_and_quantize_even_widths(dtype, T, H):
     assert ok()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("B,n", [(1, 700), (1, 60001), (296, 60001)])
+@pytest.mark.parametrize("top", [8.0, 12.5, 14.0])
+def test_paged_attn_small_weights_beside_dominant_keys(dtype, B, n, top):
+    """A few keys of weight 1 whose values are 0 among the first, the others of
+    weight e^-top each with values of 1: the output is the small weights' share.
+    The largest batch gives a block whole sequences, so that one running maximum
+    covers them."""
+    dt = TYPES[dtype]
+    page, D = 64, 64
+    P = -(-n // page)
+    kp, vp = torch.zeros(P, 1, page, D, device="cuda", dtype=dt), torch.ones(P, 1, page, D, device="cuda", dtype=dt)
+    table = torch.arange(P, dtype=torch.int32, device="cuda").view(1, P).repeat(B, 1)
+    kp[:2, :, ::16, 0] = top
+    vp[:2, :, ::16] = 0
+    q = torch.zeros(B, 6, D, device="cuda", dtype=dt)
+    q[:, :, 0] = 1
+    out, st = run_paged(q, kp, vp, table, [n] * B, scale=1.0)
+    want, tol = paged_ref(q[:1], kp, vp, table, [n], scale=1.0)
+    close(out, want.expand(B, -1, -1), tol.expand(B, -1, -1), "shares")
+    assert st == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (5, 1, 128), (12, 1, 64), (16, 1, 256), (9, 1, 128), (24, 1, 64)])
 def test_paged_attn_joins_of_many_blocks(Hq, Hkv, D):
     """One and two sequences of one KV head, long enough that every block of the
