@@ -16,6 +16,9 @@ Tolerances, per output value (h = half a step of the output type, relative):
              max_j sum |q k| the scores' error, fp32 additions n / 64 strips deep.
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -781,3 +784,79 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for *_, outs in jobs:
         assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H", [(300, 32767), (2, 32766), (700, 16384), (301, 9999), (40000, 3)])
+def test_rmsnorm_widest_rows(dtype, T, H):
+    """Rows of a whole block's warps on each path, and many of the narrowest."""
+    dt, g = TYPES[dtype], gen(T + H)
+    x, w, r = randn(g, T, H).to(dt), (1 + 0.3 * randn(g, H)).to(dt), randn(g, T, H).to(dt)
+    out, ok1 = guard(T, H, dtype=dt)
+    q, ok2 = guard(T, H, dtype=torch.float8_e4m3fn)
+    sc, so = torch.empty(T, (H + 127) // 128, device="cuda"), torch.empty_like(x)
+    ob.orthrus_rmsnorm(x, w, 1e-5, out=out, residual=r, sum_out=so, out_fp8=q, out_scale=sc)
+    s, y = norm_ref(x, r, w, 1e-5)
+    close(out, y, (half_step(dt) + 2.0 ** -18) * y.abs() + tiny(dt), "norm")
+    check_fp8(q, sc, y, "norm")
+    assert ok1() and ok2()
+
+
+@pytest.mark.parametrize("M,N,K", [(70001, 17, 64), (9000, 1, 48), (1, 1, 16), (128, 3, 12288), (129, 1, 12288)])
+@pytest.mark.parametrize("out", ["f16", "f32"])
+def test_fp8_matmul_tall_and_thin(M, N, K, out):
+    g = gen(M + N + K)
+    a, sa, w, sw = fp8_operands(g, M, N, K)
+    o, ok = guard(M, N, dtype=TYPES[out])
+    ob.orthrus_fp8_matmul(a, sa, w, sw, o)
+    check_product(o, a, sa, w, sw)
+    assert ok()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 1), (256, 17, 1), (128, 6, 2)])
+def test_paged_attn_largest_batch(D, Hq, Hkv):
+    """As many sequences as one call takes, most of them short and some empty, over
+    pages that several of them share."""
+    g = gen(D)
+    B, page, P = 4096, 8, 64
+    lens = torch.randint(0, 30, (B,), generator=g, device="cuda")
+    lens[17], lens[4000] = 500, 0
+    table = torch.randint(0, P, (B, 63), generator=g, device="cuda").int()
+    kp, vp = (randn(g, P, Hkv, page, D).bfloat16() for _ in range(2))
+    q = randn(g, B, Hq, D).bfloat16()
+    out, st = run_paged(q, kp, vp, table, lens.tolist())
+    some = [0, 1, 16, 17, 18, 2047, 2048, 3999, 4000, 4001, 4095] + torch.randint(0, B, (60,), generator=g, device="cuda").tolist()
+    want, tol = paged_ref(q[some], kp, vp, table[some], lens[some].tolist())
+    close(out[some], want, tol, "largest batch")
+    assert st == 0 and not out[lens == 0].any()
+
+
+FIRST = """
+import sys, torch
+from lossless_diffusion_speculative_b200 import binding as ob
+sys.path.insert(0, sys.argv[1])
+import test_gpu_layer_ops as t
+l = t.Layer(51)
+M, N, K = 300, 520, 256
+a, sa, w, sw = t.fp8_operands(t.gen(1), M, N, K)
+o = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    l.run()
+    ob.orthrus_fp8_matmul(a, sa, w, sw, o)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+l.check()
+t.check_product(o, a, sa, w, sw)
+print("captured first")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """No call needs one outside a capture before it."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST, here], cwd=os.path.dirname(here), capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
