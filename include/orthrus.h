@@ -488,7 +488,7 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
  *             At least one of out and out_fp8 is given.
  * Supported: H <= ORTHRUS_MAX_NORM_WIDTH, any T.  16-byte aligned pointers,
  * x_stride and H multiples of 8 take the vector path; anything else is read
- * element by element.
+ * four, two or one values at a time, as its alignment allows.
  */
 ORTHRUS_API int orthrus_rmsnorm(orthrus_dtype dtype, const void *x, int64_t x_stride,
                                 const void *residual, const void *weight, int T, int H, float eps,
