@@ -480,7 +480,8 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
  *   out_fp8   optional [T, H] e4m3, dense, with out_scale [T, ceil(H / 128)]
  *             fp32: for each group of 128 columns (the last may be short)
  *                 scale = max(max|y| / 448, 2^-126),  value = e4m3(y / scale)
- *             (nearest; the quotient is y times the fp32 reciprocal of the
+ *             (the scale as the fp32 product with the nearest value to 1 / 448;
+ *             value nearest; the quotient is y times the fp32 reciprocal of the
  *             scale, so one that lies on a border between two values can go
  *             to either), so value * scale stands for y and a group of zeros
  *             has a finite scale.  A NaN stays a NaN and does not enter

@@ -2,7 +2,7 @@
 // with scales behind it, and plain quantisation to the same 8-bit form.
 //
 //     s = x + r;  y = s * rsqrt(mean(s^2) + eps) * w
-//     scale = max(max|y| / 448, 2^-126) per 128 columns;  value = e4m3(y / scale)
+//     scale = max(max|y| (1 / 448), 2^-126) per 128 columns;  value = e4m3(y / scale)
 //
 // One pass: a row's values stay in registers (fp32) between the sum of squares
 // and the outputs, so each input is read and each output written once.  A row
@@ -48,21 +48,16 @@ __device__ __forceinline__ float lanes_max(float v, int o)
     return v;
 }
 
-// Scale of a group from its maximum, and the scale's reciprocal.  The division
-// is multiplication by the rounded reciprocal and one exact-remainder step
-// (fma), which gives the correctly rounded quotient.
+// Scale of a group from its maximum, and the scale's reciprocal (the nearest fp32
+// value; 0 for a scale of infinity, so that finite values become 0).
 struct Scale {
     float s, inv;
 };
 __device__ __forceinline__ Scale scale_of(float amax)
 {
-    const float r = 1.0f / 448.0f, q = amax * r;
     Scale o;
-    o.s = fmaxf(amax < INFINITY ? fmaf(fmaf(-q, 448.0f, amax), r, q) : amax, 1.17549435e-38f);
-    float a;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(o.s));
-    const float b = fmaf(fmaf(-o.s, a, 1.0f), a, a);
-    o.inv = o.s < INFINITY ? b : 0.f;
+    o.s = fmaxf(amax * (1.0f / 448.0f), 1.17549435e-38f);
+    o.inv = o.s < INFINITY ? __frcp_rn(o.s) : 0.f;
     return o;
 }
 
