@@ -481,11 +481,9 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
  *             fp32: for each group of 128 columns (the last may be short)
  *                 scale = max(max|y| / 448, 2^-126),  value = e4m3(y / scale)
  *             (the scale as the fp32 product with the nearest value to 1 / 448;
- *             value nearest; the quotient is y times the fp32 reciprocal of the
- *             scale, so one that lies on a border between two values can go
- *             to either), so value * scale stands for y and a group of zeros
- *             has a finite scale.  A NaN stays a NaN and does not enter
- *             the maximum.
+ *             the nearest fp32 quotient, rounded to the nearest e4m3 value), so
+ *             value * scale stands for y and a group of zeros has a finite scale.
+ *             A NaN stays a NaN and does not enter the maximum.
  *             At least one of out and out_fp8 is given.
  * Supported: H <= ORTHRUS_MAX_NORM_WIDTH, any T.  16-byte aligned pointers,
  * x_stride and H multiples of 8 take the vector path; anything else is read

@@ -49,7 +49,8 @@ __device__ __forceinline__ float lanes_max(float v, int o)
 }
 
 // Scale of a group from its maximum, and the scale's reciprocal (the nearest fp32
-// value; 0 for a scale of infinity, so that finite values become 0).
+// value), or 0 from 2^80 on, where the reciprocal's own error would fall below the
+// smallest numbers, and for a scale of infinity.
 struct Scale {
     float s, inv;
 };
@@ -57,8 +58,18 @@ __device__ __forceinline__ Scale scale_of(float amax)
 {
     Scale o;
     o.s = fmaxf(amax * (1.0f / 448.0f), 1.17549435e-38f);
-    o.inv = o.s < INFINITY ? __frcp_rn(o.s) : 0.f;
+    o.inv = o.s < 0x1p80f ? __frcp_rn(o.s) : 0.f;
     return o;
+}
+
+// Where inv is 0: a factor for the group's values that keeps their quotients by
+// the scale, which is changed with them (finite / infinity: zeros).
+__device__ __forceinline__ float lower(Scale &sc)
+{
+    const bool finite = sc.s < INFINITY;
+    sc.s = finite ? sc.s * 0x1p-100f : 1.0f;
+    sc.inv = __frcp_rn(sc.s);
+    return finite ? 0x1p-100f : 0.f;
 }
 
 // Maxima of NC chunks' values over 16 lanes, as scales: the butterfly folds chunks
@@ -97,14 +108,25 @@ template <int NC> __device__ __forceinline__ void scales_of(const float (&m)[NC]
     }
 }
 
-// y / scale as e4m3: two values, low byte first.  The quotient is y times the
-// rounded reciprocal, up to 1.5 units in fp32's last place off: a quotient that
-// lies on a border between two e4m3 values can go to either.  (The remainder
-// step that would round it correctly costs two FMAs a pair, and at the board's
-// power limit 10 % of the time: 58.6 against 52.8 us at 8192 x 12288.)
-__device__ __forceinline__ uint32_t quotient2(float2 y, const Scale &sc)
+// 1 / s as the nearest fp32 value and the rest: together good to 2^-48 (1 - s inv is
+// exact, an fma).
+struct Inverse {
+    float2 hi, lo;
+};
+__device__ __forceinline__ Inverse inverse_of(const Scale &sc)
 {
-    return __nv_cvt_float2_to_fp8x2(sm100::fmul2(y, make_float2(sc.inv, sc.inv)), __NV_SATFINITE, __NV_E4M3);
+    const float rest = fmaf(-sc.s, sc.inv, 1.0f) * sc.inv;
+    return {make_float2(sc.inv, sc.inv), make_float2(rest, rest)};
+}
+
+// y / scale as e4m3: two values, low byte first.  The quotient is rounded to fp32
+// once, from y (hi + lo) within 2^-47 of it: 16-bit inputs lie on the borders
+// between two e4m3 values often, and a quotient that is one fp32 step off can go to
+// the wrong neighbour there (with y hi alone 21 of 8192 x 12288 bf16 values did).
+// At every border the result equals the division's, for every significand of a scale.
+__device__ __forceinline__ uint32_t quotient2(float2 y, const Inverse &v)
+{
+    return __nv_cvt_float2_to_fp8x2(sm100::ffma2(y, v.hi, sm100::fmul2(y, v.lo)), __NV_SATFINITE, __NV_E4M3);
 }
 
 // ---- vector path
@@ -220,11 +242,18 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const NormArgs p)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int k = k0 + c * W * 256;
-                const uint32_t lo = quotient2(s[c][0], sc[c]) | (quotient2(s[c][1], sc[c]) << 16);
-                const uint32_t hi = quotient2(s[c][2], sc[c]) | (quotient2(s[c][3], sc[c]) << 16);
+                const float scale = sc[c].s;
+                if (sc[c].inv == 0.f) {
+                    const float f = lower(sc[c]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[c][j] = sm100::fmul2(s[c][j], make_float2(f, f));
+                }
+                const Inverse v = inverse_of(sc[c]);
+                const uint32_t lo = quotient2(s[c][0], v) | (quotient2(s[c][1], v) << 16);
+                const uint32_t hi = quotient2(s[c][2], v) | (quotient2(s[c][3], v) << 16);
                 if (live && k < H) {
                     *reinterpret_cast<uint2 *>(p.out_fp8 + (int64_t)r * H + k) = make_uint2(lo, hi);
-                    if ((lane & 15) == 0) p.out_scale[(int64_t)r * groups + (k >> 7)] = sc[c].s;
+                    if ((lane & 15) == 0) p.out_scale[(int64_t)r * groups + (k >> 7)] = scale;
                 }
             }
         }
@@ -326,13 +355,20 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
                 float m = 0.f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(s[c][4 * h + j]));
-                const Scale sc = scale_of(lanes_max(m, 16));
+                Scale sc = scale_of(lanes_max(m, 16));
+                const float scale = sc.s;
                 if (!live) continue;
+                if (sc.inv == 0.f) {
+                    const float f = lower(sc);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[c][4 * h + j] *= f;
+                }
+                const Inverse inv = inverse_of(sc);
 #pragma unroll
                 for (int j = 4 * h; j < 4 * h + 4; j += V == 4 ? 4 : 2) {
-                    const uint32_t v = quotient2(make_float2(s[c][j], s[c][j + 1]), sc);
+                    const uint32_t v = quotient2(make_float2(s[c][j], s[c][j + 1]), inv);
                     if constexpr (V == 4) {
-                        const uint32_t hi = quotient2(make_float2(s[c][j + 2], s[c][j + 3]), sc);
+                        const uint32_t hi = quotient2(make_float2(s[c][j + 2], s[c][j + 3]), inv);
                         if (col(c, h) < H) *reinterpret_cast<uint32_t *>(o + col(c, h)) = v | hi << 16;
                     } else if constexpr (V == 2) {
                         if (col(c, j / 2) < H) *reinterpret_cast<uint16_t *>(o + col(c, j / 2)) = (uint16_t)v;
@@ -341,7 +377,7 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
                         if (col(c, j + 1) < H) o[col(c, j + 1)] = (uint8_t)(v >> 8);
                     }
                 }
-                if (lane == 0 && (g0 + h) * 128 < H) os[g0 + h] = sc.s;
+                if (lane == 0 && (g0 + h) * 128 < H) os[g0 + h] = scale;
             }
         }
     }

@@ -2,7 +2,11 @@
 
 8-bit scales   bitwise equal to the fp32 product of the group's largest value and
                the nearest value to 1 / 448: no tolerance.
+8-bit values   bitwise equal to the fp32 division by the scale, rounded once to
+               e4m3: no tolerance.
 """
+import math
+
 import pytest
 import torch
 
@@ -37,10 +41,78 @@ def test_quantize_scales_are_the_rounded_products(dtype, T, H):
     assert torch.equal(quantized(x)[1], plain_scales(x))
 
 
-@pytest.mark.parametrize("e", [-149, -130, -118, -100, -80, -72, -40, 0, 60, 126])
+@pytest.mark.parametrize("e", [-149, -130, -118, -100, -80, -72, -40, 0, 60, 87, 89, 126])
 def test_quantize_scales_over_the_exponent_range(e):
     """Groups whose largest value lies around 2^e: subnormal numbers, scales at
     and near their floor, and up to the type's largest values."""
     g = gen(e + 200)
     x = torch.ldexp(randn(g, 300, 384).clamp(-3.9, 3.9).double(), torch.tensor(e, device="cuda")).clamp(-3.4e38, 3.4e38).float()
     assert torch.equal(quantized(x)[1], plain_scales(x))
+
+
+def plain_values(x, scale):
+    T, H = x.shape
+    q = x.float() / scale.repeat_interleave(128, 1)[:, :H]
+    return q.clamp(-448, 448).to(torch.float8_e4m3fn)
+
+
+def check_values(q, want):
+    """The same bits (but for the sign of a zero)."""
+    differ = (q.view(torch.uint8) != want.view(torch.uint8)) & ~((q.float() == 0) & (want.float() == 0))
+    assert not differ.any(), f"{int(differ.sum())} of {differ.numel()} values differ"
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H", [(1, 1), (32, 4096), (700, 1000), (900, 1422), (300, 1001), (5, 128)])
+def test_quantize_values_are_the_rounded_quotients(dtype, T, H):
+    g = gen(T + H)
+    x = (randn(g, T, H) * torch.exp(0.7 * randn(g, H))).to(TYPES[dtype])
+    q, sc = quantized(x)
+    check_values(q, plain_values(x, sc))
+
+
+@pytest.mark.parametrize("width", [384, 383, 382])
+@pytest.mark.parametrize("e", [-149, -130, -118, -100, -80, -72, -40, 0, 60, 87, 89, 126])
+def test_quantize_values_over_the_exponent_range(e, width):
+    g = gen(e + 200)
+    x = torch.ldexp(randn(g, 300, width).clamp(-3.9, 3.9).double(), torch.tensor(e, device="cuda")).clamp(-3.4e38, 3.4e38).float()
+    q, sc = quantized(x)
+    check_values(q, plain_values(x, sc))
+
+
+def borders(seed, groups, e):
+    """[groups, 128]: values on and up to two steps beside the borders between
+    neighbouring e4m3 values (of each significand, below 2^-6 as well), times
+    scales of any significand."""
+    g = gen(seed)
+    amax = torch.ldexp(1 + torch.rand(groups, generator=g, device="cuda", dtype=torch.float64), torch.tensor(e, device="cuda")).float()
+    s = plain_scales(amax[:, None])
+    odd = torch.arange(8, device="cuda")
+    m = torch.cat([(17 + 2 * odd) / 16, (1 + 2 * odd) * 2.0 ** -10, (17 + 2 * odd) * 4.0])
+    y = (m.double() * s.double()).float()
+    out, lo, hi = [y], y, y
+    for _ in range(2):
+        lo, hi = torch.nextafter(lo, torch.full_like(lo, -math.inf)), torch.nextafter(hi, torch.full_like(hi, math.inf))
+        out += [lo, hi]
+    return torch.cat([*out, -y[:, :7], amax[:, None]], 1).contiguous()
+
+
+@pytest.mark.parametrize("e", [-125, -110, -70, -1, 0, 87, 88, 100, 126])
+def test_quantize_values_at_every_border(e):
+    x = borders(e + 200, 40000, e)
+    q, sc = quantized(x)
+    check_values(q, plain_values(x, sc))
+
+
+def test_norm_values_are_the_rounded_quotients():
+    """Rows whose norm is exact (entries of magnitude 1, eps 0), with weights on
+    the borders."""
+    for width in (128, 2048):
+        for seed in range(40):
+            w = borders(seed, width // 128, -1).flatten()
+            g = gen(seed)
+            x = torch.where(torch.rand(9, width, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+            q, sc = torch.empty(9, width, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(9, width // 128, device="cuda")
+            ob.orthrus_rmsnorm(x, w, 0.0, out_fp8=q, out_scale=sc)
+            assert torch.equal(sc, plain_scales(x * w))
+            check_values(q, plain_values(x * w, sc))
