@@ -639,8 +639,9 @@ ORTHRUS_API int orthrus_rope_append(orthrus_dtype dtype, orthrus_rope_layout lay
  *   workspace >= orthrus_paged_attn_workspace_size(B, Hq, Hkv, D) bytes,
  *             16-byte aligned, zero-filled once before first use; every call
  *             leaves its counters zero (the rest is scratch).  The size does
- *             not depend on lengths or pages.  Calls that overlap on the device
- *             must not share it.
+ *             not depend on lengths or pages.  Calls of different shapes and
+ *             types may share a workspace that is large enough for each, one
+ *             after another; calls that overlap on the device must not.
  * Supported: D 64, 128 or 256; Hq % Hkv == 0; B <= 4096; any page_size.  q, the
  * pages and the workspace 16-byte aligned.
  * Numerics: products of 16-bit values are exact in fp32; the softmax weights

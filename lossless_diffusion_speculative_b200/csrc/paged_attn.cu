@@ -23,7 +23,9 @@
 // own cp.async ring and its own running maximum and sum (no block-wide barrier
 // inside a segment); the four are combined through shared memory when the block
 // leaves a segment.  A segment that spans blocks is joined by the last of them
-// to arrive (a counter per segment), which adds the partials in block order.
+// to arrive, which adds the partials in block order.  Its counter is the one of its
+// first block (a block leaves at most one segment unfinished), so the counters'
+// place does not depend on a call's shape: calls of any shapes can share a workspace.
 //
 // Numerics: q.k in fp32 from exact products, running maximum with a lazy
 // rescale (only when a row's maximum grows by more than 2^8), p = 2^(s - m) split
@@ -56,7 +58,7 @@ struct Args {
     const void *q, *k_pages, *v_pages;
     const int32_t *block_table, *ctx_lens;
     void *out;
-    int32_t *counters;                           // [B * segments], zero between calls
+    int32_t *counters;                           // [2 * SMs], zero between calls
     float *part_ml;                              // [2 * grid][kRows][2]: maximum, sum
     float *part_o;                               // [2 * grid][rows][D], not normalised
     int32_t *status;
@@ -631,12 +633,12 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
             if (!whole) {
                 // blocks [c0, c1] hold the segment; the last to arrive joins it
                 const int c_first = (int)(((s0 + 1) * P - 1) / total), c_last = (int)(((s0 + seg_.n) * P - 1) / total);
-                const int seg = seg_.b * segs + seg_.g, n = c_last - c_first + 1;
+                const int n = c_last - c_first + 1;
                 __syncthreads();                   // every partial store of the block, before the release
                 if (threadIdx.x == 0) {
-                    const int old = counter_fetch_add_acq_rel(p.counters + seg, 1);
+                    const int old = counter_fetch_add_acq_rel(p.counters + c_first, 1);
                     flag = old == n - 1;
-                    if (flag) p.counters[seg] = 0;
+                    if (flag) p.counters[c_first] = 0;
                 }
                 __syncthreads();
                 if (flag) {
@@ -658,21 +660,23 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
     cp_wait<0>();
 }
 
-// Largest page-table geometry and the block count the launch uses.
+// The launch's block count.
 inline int grid_of(int D, int sms) { return D == 256 ? sms : 2 * sms; }
 
 struct Plan {
     int grid;
-    size_t counters, ml, o, total;
+    size_t ml, o, total;                         // partials' places; the counters come first
 };
 
+// The counters sit at the same place for every shape; the partials, which may lie
+// anywhere behind them, leave a word per segment free at the head as well.
 inline Plan plan(int B, int Hq, int Hkv, int D, int sms)
 {
     Plan w;
     const int G = Hq / Hkv, HG = (G + kRows - 1) / kRows;
     w.grid = grid_of(D, sms);
-    w.counters = ((size_t)B * Hkv * HG * sizeof(int32_t) + 255) & ~(size_t)255;
-    w.ml = w.counters;
+    const size_t words = (size_t)B * Hkv * HG, counters = 2 * (size_t)sms;
+    w.ml = ((words > counters ? words : counters) * sizeof(int32_t) + 255) & ~(size_t)255;
     w.o = w.ml + (((size_t)2 * w.grid * kRows * 2 * sizeof(float) + 255) & ~(size_t)255);
     w.total = w.o + (size_t)2 * w.grid * kRows * D * sizeof(float);
     return w;

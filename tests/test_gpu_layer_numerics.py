@@ -4,6 +4,7 @@
                the nearest value to 1 / 448: no tolerance.
 8-bit values   bitwise equal to the fp32 division by the scale, rounded once to
                e4m3: no tolerance.
+Attention of mixed shapes: the bound that test_gpu_layer_ops.py derives.
 """
 import math
 
@@ -11,7 +12,7 @@ import pytest
 import torch
 
 from lossless_diffusion_speculative_b200 import binding as ob
-from test_gpu_layer_ops import TYPES, gen, randn
+from test_gpu_layer_ops import TYPES, close, gen, paged_cache, paged_ref, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +117,32 @@ def test_norm_values_are_the_rounded_quotients():
             ob.orthrus_rmsnorm(x, w, 0.0, out_fp8=q, out_scale=sc)
             assert torch.equal(sc, plain_scales(x * w))
             check_values(q, plain_values(x * w, sc))
+
+
+# ------------------------------------------------------------------- attention
+def test_paged_attn_shapes_share_a_workspace():
+    """Calls of different shapes and types through one workspace of the largest
+    size, small ones before large ones and back: segments over many blocks, so
+    that a counter that is not zero at its call shows as rows not written."""
+    g = gen(61)
+    shapes = [  # dtype, Hq, Hkv, D, page, lengths
+        ("bf16", 8, 8, 128, 32, [20000]),
+        ("bf16", 32, 8, 128, 16, [3000 + 37 * i for i in range(32)]),
+        ("f16", 16, 2, 64, 8, [9000, 1, 0, 777]),
+        ("bf16", 4, 1, 256, 64, [30000, 5]),
+        ("bf16", 40, 2, 128, 16, [500 * i for i in range(20)]),
+        ("f16", 6, 2, 64, 16, [i % 50 for i in range(700)]),
+        ("bf16", 24, 8, 64, 128, [40000, 20000, 3])]
+    calls = []
+    for dtype, Hq, Hkv, D, page, lens in shapes:
+        dt = TYPES[dtype]
+        kp, vp, table = paged_cache(g, lens, page, Hkv, D, dt)
+        q = randn(g, len(lens), Hq, D).to(dt)
+        calls.append((q, kp, vp, table, lens, *paged_ref(q, kp, vp, table, lens)))
+    size = max(ob.orthrus_paged_attn_workspace_size(q.shape[0], q.shape[1], kp.shape[1], q.shape[2]) for q, kp, *_ in calls)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for i in [0, 1, 0, 2, 1, 3, 4, 5, 0, 6, 5, 2, 4, 3, 1, 6]:
+        q, kp, vp, table, lens, want, tol = calls[i]
+        out = torch.full_like(q, math.nan)
+        ob.orthrus_paged_attn(q, kp, vp, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, ws)
+        close(out, want, tol, f"shape {i}")
