@@ -335,8 +335,11 @@ def orthrus_prefill_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
 # few attribute reads per tensor cost.)
 _CODES = {torch.bfloat16: BF16, torch.float32: F32, torch.float16: F16}
 _E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (torch's own short forms of these two look-ups; a torch built without CUDA has
+# neither, and the package is imported there too)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _code(dt: torch.dtype) -> int:
