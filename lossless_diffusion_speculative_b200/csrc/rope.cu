@@ -5,8 +5,8 @@
 // For pair i of the first rot elements of a head at position t:
 //     (a, b) <- m (a cos p - b sin p, b cos p + a sin p),  p = 2 pi frac(t * turns_i)
 // The product t * turns_i and its fraction are fp64: at position 2^20 an fp32
-// angle would be off by 2^-4 radians.  sincospi then gets an fp32 fraction in
-// [-1, 1], good to 2^-24 of a half turn.
+// angle would be off by 2^-4 radians.  sincospi gets an fp32 fraction in [-1, 1]
+// of a half turn, and what its rounding lost is added to first order.
 //
 // Vector path: a warp takes a token and a run of its heads, LP lanes of 16
 // values each per head.  A lane's two 8-value vectors are the two sides of 8
@@ -109,13 +109,15 @@ __device__ __forceinline__ bool item_of(const RopeArgs &p, int t, int h, int64_t
     return true;
 }
 
+// The fp32 fraction's rest d, up to pi 2^-25 radians, turns the pair by itself
+// (its square is below 2^-46).
 __device__ __forceinline__ float2 cos_sin(const RopeArgs &p, int pos, int i)
 {
-    const double turn = (double)pos * p.turns[i];
-    const float f = (float)(2.0 * (turn - rint(turn)));
+    const double turn = (double)pos * p.turns[i], half_turns = 2.0 * (turn - rint(turn));
+    const float f = (float)half_turns, d = (float)(half_turns - (double)f) * 3.14159265f;
     float s, c;
     sincospif(f, &s, &c);
-    return make_float2(c * p.magnitude, s * p.magnitude);
+    return make_float2(fmaf(-s, d, c) * p.magnitude, fmaf(c, d, s) * p.magnitude);
 }
 
 constexpr int kRopeThreads = 256;

@@ -146,3 +146,25 @@ def test_paged_attn_shapes_share_a_workspace():
         out = torch.full_like(q, math.nan)
         ob.orthrus_paged_attn(q, kp, vp, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, ws)
         close(out, want, tol, f"shape {i}")
+
+
+# -------------------------------------------------------------------- rotation
+@pytest.mark.parametrize("rot,D", [(64, 64), (128, 128), (10, 20), (6, 33)])
+@pytest.mark.parametrize("layout", [ob.ROPE_HALF, ob.ROPE_INTERLEAVED])
+def test_rope_sines_and_cosines_to_the_last_bits(rot, D, layout):
+    """Pairs (1, 0) in fp32 come back as (cos, sin): within two steps for the
+    function and half a step for the angle's last bits, at any position."""
+    pos = torch.arange(0, 1 << 20, 97, dtype=torch.int32, device="cuda")
+    turns = ob.orthrus_rope_table(rot, 1e4)[0].cuda()
+    h = rot // 2
+    ia = torch.arange(h, device="cuda") * (2 if layout == ob.ROPE_INTERLEAVED else 1)
+    ib = ia + (1 if layout == ob.ROPE_INTERLEAVED else h)
+    x = torch.zeros(pos.numel(), 1, D, device="cuda")
+    x[..., ia] = 1
+    out = torch.empty_like(x)
+    ob.orthrus_rope(x, None, pos, turns, out, layout=layout)
+    t = pos.double()[:, None] * turns
+    ang = 2 * math.pi * (t - t.round())
+    for at, want in ((ia, ang.cos()), (ib, ang.sin())):
+        # (a step of fp32 is at most 2^-23 of the value; the angle's second order, 64 bits)
+        close(out[:, 0, at], want, 2.5 * 2.0 ** -23 * want.abs() + 1e-13, "turn")
