@@ -645,7 +645,8 @@ ORTHRUS_API int orthrus_rope_append(orthrus_dtype dtype, orthrus_rope_layout lay
  * Supported: D 64, 128 or 256; Hq % Hkv == 0; B <= 4096; any page_size.  q, the
  * pages and the workspace 16-byte aligned.
  * Numerics: products of 16-bit values are exact in fp32; the softmax weights
- * enter the second product as two 16-bit terms, the statistics are fp32, the
+ * enter the second product as three bf16 terms (24 bits) or two fp16 ones (22
+ * bits, and 2^-32 of the largest weight), the statistics are fp32, the
  * splits are joined in a fixed order (results do not depend on timing).
  */
 ORTHRUS_API size_t orthrus_paged_attn_workspace_size(int B, int Hq, int Hkv, int D);

@@ -29,8 +29,10 @@
 //
 // Numerics: q.k in fp32 from exact products, running maximum with a lazy
 // rescale (only when a row's maximum grows by more than 2^8), p = 2^(s - m) split
-// into two 16-bit terms p_hi + p_lo for the second product: one 16-bit p would
-// lose 2^-9 (bf16) per weight, the second term is free behind the stream.  fp16
+// into 16-bit terms for the second product: three of bf16, which hold all of p's 24
+// bits, or two of fp16, 22 bits.  (The third of bf16 hides behind the stream for up
+// to 8 heads: 168.8 and 169.1 us for 8 long sequences; 16 heads take 61.2 and 63.5
+// us, of 256 values 126 and 138.)  fp16
 // weights are held 2^7 up (2^15 at most): a step of 2^-24 at the bottom of the
 // type's range, against a largest weight of 1, lost up to 0.8 % of the many small
 // weights of a long cache beside one dominant key.
@@ -113,6 +115,31 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// Two weights as sums of 16-bit terms, each term's two values packed.
+template <typename T> struct Split;
+template <> struct Split<__nv_bfloat16> {
+    static constexpr int terms = 3;                                  // truncated: 8 bits each, exact together
+    static __device__ __forceinline__ void of(float a, float b, uint32_t (&w)[3])
+    {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+            w[i] = __byte_perm(x, y, 0x7632);
+            a -= __uint_as_float(x & 0xffff0000u);
+            b -= __uint_as_float(y & 0xffff0000u);
+        }
+    }
+};
+template <> struct Split<__half> {
+    static constexpr int terms = 2;
+    static __device__ __forceinline__ void of(float a, float b, uint32_t (&w)[2])
+    {
+        w[0] = pack2<__half>(a, b);
+        const float2 back = unpack2<__half>(w[0]);
+        w[1] = pack2<__half>(a - back.x, b - back.y);
+    }
+};
 
 // Position in the flat tile order: sequence b, segment g (KV head x head
 // group), tile t of its n tiles.
@@ -530,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                     }
                 }
             }
-            uint32_t hi_[NS][NH][2], lo_[NS][NH][2];
+            constexpr int TERMS = Split<T>::terms;
+            uint32_t pw[TERMS][NS][NH][2];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 // a head whose scores so far are all -inf keeps the weights at zero
@@ -543,10 +571,10 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                         const float x1 = fast_exp2(fmaf(s[i][h][2 * k + 1], p.scale_log2, -e1));
                         l[h][0] += x0;
                         l[h][1] += x1;
-                        const uint32_t w = pack2<T>(x0, x1);
-                        const float2 back = unpack2<T>(w);
-                        hi_[i][h][k] = transpose8(w);
-                        lo_[i][h][k] = transpose8(pack2<T>(x0 - back.x, x1 - back.y));
+                        uint32_t w[TERMS];
+                        Split<T>::of(x0, x1, w);
+#pragma unroll
+                        for (int t = 0; t < TERMS; ++t) pw[t][i][h][k] = transpose8(w[t]);
                     }
                 }
             }
@@ -559,10 +587,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 1 : 2) paged_attn_kernel(
                     uint32_t v[4];
                     ldsm4_t(v, sv + (i * 16 + r) * D * 2 + (((2 * d + cc) ^ (r & 7)) << 4));
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        mma<T>(o[d][h], v, hi_[i][h][0], hi_[i][h][1]);
-                        mma<T>(o[d][h], v, lo_[i][h][0], lo_[i][h][1]);
-                    }
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int t = 0; t < TERMS; ++t) mma<T>(o[d][h], v, pw[t][i][h][0], pw[t][i][h][1]);
                 }
             }
         }

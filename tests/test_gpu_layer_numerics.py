@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from lossless_diffusion_speculative_b200 import binding as ob
-from test_gpu_layer_ops import TYPES, close, gen, paged_cache, paged_ref, randn
+from test_gpu_layer_ops import TYPES, close, gen, half_step, paged_cache, paged_ref, randn, run_paged, tiny
 
 pytestmark = pytest.mark.gpu
 
@@ -146,6 +146,32 @@ def test_paged_attn_shapes_share_a_workspace():
         out = torch.full_like(q, math.nan)
         ob.orthrus_paged_attn(q, kp, vp, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), out, ws)
         close(out, want, tol, f"shape {i}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_paged_attn_weights_keep_24_bits(dtype, D):
+    """Two keys of weight 1 whose values cancel a third key's share p to about
+    2^-18 of it (bf16; fp16 2^-24): what is left shows p's own bits.  Tolerance, in
+    2^-24 p: exp2 to 2^-22 twice (4 + 4), its argument's rounding (at most 8 after
+    fp16's offset of 7, and 2.9 for the factor log2 e, times ln 2: 7.5), eight fp32
+    additions of at most p (8, truncated)."""
+    dt = TYPES[dtype]
+    k = torch.arange(64, 192, device="cuda") * -2.0 ** -7                         # -0.5 .. -1.5
+    B = k.numel()
+    p = k.double().exp()
+    a1 = p.to(dt)
+    a2 = (p - a1.double()).to(dt)
+    kp, vp = (torch.zeros(B, 1, 4, D, dtype=dt, device="cuda") for _ in range(2))
+    kp[:, 0, 2, 0] = k.to(dt)
+    vp[:, 0, 0], vp[:, 0, 1], vp[:, 0, 2] = -a1[:, None], -a2[:, None], 1
+    q = torch.zeros(B, 2, D, dtype=dt, device="cuda")
+    q[..., 0] = 1
+    out, st = run_paged(q, kp, vp, torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1), [3] * B, scale=1.0)
+    want = (p - a1.double() - a2.double()) / (2 + p)
+    tol = half_step(dt) * want.abs() + 24 * 2.0 ** -24 * p / (2 + p) + tiny(dt)
+    close(out, want[:, None, None].expand_as(out), tol[:, None, None], "weights")
+    assert st == 0
 
 
 # -------------------------------------------------------------------- rotation
