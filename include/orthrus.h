@@ -623,7 +623,8 @@ ORTHRUS_API int orthrus_rope_append(orthrus_dtype dtype, orthrus_rope_layout lay
  *
  *     out[b, h, :] = sum_j softmax_j(scale * <q[b,h,:], K[b,g,j,:]>) V[b,g,j,:]
  * over j in [0, ctx_lens[b] + n_new), g = h / (Hq / Hkv).  A sequence with no
- * visible key gives zeros.
+ * visible key gives zeros.  An infinite value of a visible key stays that
+ * infinity in the output (with a weight below 2^-32 of the largest, a NaN).
  *
  *   dtype     ORTHRUS_BF16 or ORTHRUS_F16, of q, the pages and out.
  *   q, out    [B, Hq, D], dense.

@@ -116,15 +116,23 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two weights as sums of 16-bit terms, each term's two values packed.
+// Two weights as sums of 16-bit terms, each term's two values packed.  Every term
+// but the last is the largest value below what it stands for, so that none is zero
+// or negative beside a weight that is not, and an infinite value of a key stays the
+// infinity it is (0 times it would be a NaN).  (Up to 1 % of a call's time.)
+__device__ __forceinline__ float below(float x)          // x >= 0; 0 stays
+{
+    const uint32_t u = __float_as_uint(x);
+    return __uint_as_float(u - (u < 1u ? u : 1u));
+}
 template <typename T> struct Split;
 template <> struct Split<__nv_bfloat16> {
-    static constexpr int terms = 3;                                  // truncated: 8 bits each, exact together
+    static constexpr int terms = 3;                      // truncated to 8 bits each, exact together
     static __device__ __forceinline__ void of(float a, float b, uint32_t (&w)[3])
     {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+            const uint32_t x = __float_as_uint(i < 2 ? below(a) : a), y = __float_as_uint(i < 2 ? below(b) : b);
             w[i] = __byte_perm(x, y, 0x7632);
             a -= __uint_as_float(x & 0xffff0000u);
             b -= __uint_as_float(y & 0xffff0000u);
@@ -135,7 +143,8 @@ template <> struct Split<__half> {
     static constexpr int terms = 2;
     static __device__ __forceinline__ void of(float a, float b, uint32_t (&w)[2])
     {
-        w[0] = pack2<__half>(a, b);
+        const __half2 h = __halves2half2(__float2half_rz(below(a)), __float2half_rz(below(b)));
+        w[0] = *reinterpret_cast<const uint32_t *>(&h);
         const float2 back = unpack2<__half>(w[0]);
         w[1] = pack2<__half>(a - back.x, b - back.y);
     }

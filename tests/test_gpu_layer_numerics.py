@@ -174,6 +174,31 @@ def test_paged_attn_weights_keep_24_bits(dtype, D):
     assert st == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,lens", [(64, [40]), (128, [9, 5000]), (256, [300, 20000])])
+def test_paged_attn_infinite_values(dtype, D, lens):
+    """A visible key with weight and an infinite value: infinity in that place of
+    the output, nothing elsewhere; both signs meet in a NaN."""
+    dt, page, Hq = TYPES[dtype], 16, 4
+    g = gen(D)
+    P = sum(-(-n // page) for n in lens)
+    table = torch.full((len(lens), -(-max(lens) // page)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(lens):
+        c = -(-n // page)
+        table[b, :c] = torch.arange(at, at + c, dtype=torch.int32)
+        at += c
+    kp, vp = randn(g, P, 1, page, D).to(dt) / 8, randn(g, P, 1, page, D).to(dt)
+    for b, n in enumerate(lens):
+        for d, j, v in ((3, n // 2, math.inf), (5, n - 1, -math.inf), (7, 0, math.inf), (7, n - 1, -math.inf)):
+            vp[int(table[b, j // page]), 0, j % page, d] = v
+    q = randn(g, len(lens), Hq, D).to(dt)
+    out, st = run_paged(q, kp, vp, table.cuda(), lens)
+    assert (out[..., 3] == math.inf).all() and (out[..., 5] == -math.inf).all() and out[..., 7].isnan().all()
+    rest = [d for d in range(D) if d not in (3, 5, 7)]
+    assert out[..., rest].isfinite().all() and st == 0
+
+
 # -------------------------------------------------------------------- rotation
 @pytest.mark.parametrize("rot,D", [(64, 64), (128, 128), (10, 20), (6, 33)])
 @pytest.mark.parametrize("layout", [ob.ROPE_HALF, ob.ROPE_INTERLEAVED])
