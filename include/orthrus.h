@@ -498,7 +498,7 @@ ORTHRUS_API int orthrus_rmsnorm(orthrus_dtype dtype, const void *x, int64_t x_st
  * orthrus_quantize_fp8 — x [T, H] of dtype (rows x_stride apart) to e4m3 with a
  * scale per row and group of 128 columns, as out_fp8 / out_scale above with y =
  * x: the inputs of 8-bit products that no norm produces (attention output,
- * gated activations).  Any H.
+ * gated activations).  H up to 2^30.
  */
 ORTHRUS_API int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t x_stride, int T,
                                      int H, void *out_fp8, float *out_scale, void *stream);

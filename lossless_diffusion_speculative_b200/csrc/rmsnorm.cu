@@ -486,6 +486,7 @@ extern "C" int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t 
 {
     if (!x || !out_fp8 || !out_scale || !elem_size(dtype) || T <= 0 || H <= 0) return ORTHRUS_ERR_ARG;
     if (x_stride < (T > 1 ? H : 0)) return ORTHRUS_ERR_ARG;
+    if (H > 1 << 30) return ORTHRUS_ERR_UNSUPPORTED;                                     // (columns are 32-bit)
     NormArgs a = {x, nullptr, nullptr, x_stride, nullptr, nullptr, static_cast<uint8_t *>(out_fp8), out_scale, T, H, 1, 0.f};
     if ((int64_t)T * ((H + 255) / 256) >= (1ll << 31)) return ORTHRUS_ERR_UNSUPPORTED;   // (units of work are 32-bit)
     return norm_call<false>(dtype, a, stream);
