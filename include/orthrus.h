@@ -516,7 +516,7 @@ ORTHRUS_API int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t
  *            (one scale per 128 x 128 block; short blocks at the ends).
  *   out      [M, N] of out_dtype, dense.
  *   status   optional device int32 (ORTHRUS_STATUS_TIMEOUT only).
- * Supported: M and N up to 2^30, K a multiple of 16; a and w 16-byte aligned (their
+ * Supported: M, N and K up to 2^30, K a multiple of 16; a and w 16-byte aligned (their
  * rows are then too), out aligned to its element; sm_100 devices only.  No
  * workspace: results do not depend on scheduling and calls may overlap.
  */

@@ -530,7 +530,7 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     if (!a || !a_scale || !w || !w_scale || !out || M <= 0 || N <= 0 || K <= 0) return ORTHRUS_ERR_ARG;
     const int e = elem_size(out_dtype);
     if (!e) return ORTHRUS_ERR_ARG;
-    if (K % 16 || M > 1 << 30 || N > 1 << 30) return ORTHRUS_ERR_UNSUPPORTED;
+    if (K % 16 || K > 1 << 30 || M > 1 << 30 || N > 1 << 30) return ORTHRUS_ERR_UNSUPPORTED;
     if (((uintptr_t)a | (uintptr_t)w) & 15u) return ORTHRUS_ERR_ALIGN;
     if (((uintptr_t)out & (uintptr_t)(e - 1)) || (((uintptr_t)a_scale | (uintptr_t)w_scale) & 3u)) return ORTHRUS_ERR_ALIGN;
     int dev = 0, sms = 0, major = 0;

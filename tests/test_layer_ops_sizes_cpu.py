@@ -20,3 +20,9 @@ def test_quantize_refuses_rows_past_32_bit_columns(lib):
     for dtype in (ob.BF16, ob.F16, ob.F32):
         for H in ((1 << 30) + 1, (1 << 31) - 1024, (1 << 31) - 1):
             assert lib.orthrus_quantize_fp8(dtype, P, H, 1, H, P, P, None) == ob.ERR_UNSUPPORTED
+
+
+def test_product_refuses_sizes_past_32_bits(lib):
+    f = lib.orthrus_fp8_matmul
+    for M, N, K in ((4, 64, (1 << 30) + 16), (4, 64, (1 << 31) - 16), (300, 600, (1 << 31) - 128)):
+        assert f(P, P, P, P, M, N, K, ob.BF16, P, None, None) == ob.ERR_UNSUPPORTED
