@@ -552,10 +552,12 @@ extern "C" int orthrus_fp8_matmul(const void *a, const float *a_scale, const voi
     if (M <= 16) return f8::launch_rows<16, 4, 3>(p, a, w, dev, st);
     if (M <= 32) return f8::launch_rows<32, 4, 2>(p, a, w, dev, st);
     if (M <= 64) return f8::launch_rows<64, 2, 3>(p, a, w, dev, st);
-    // Pairs from 129 rows on, unless their 256 x 256 tiles (no K split) leave most
-    // SMs idle: 256 x 4096 x 12288 (16 tiles) takes 30 us by rows and 54 by pairs,
-    // 256 x 6144 x 4096 (24) 22 and 22, 512 x 6144 x 4096 (48) 40 and 23.
-    const int64_t pair_tiles = (int64_t)((M + 255) / 256) * ((N + f8::kPairN - 1) / f8::kPairN);
-    if (M <= 128 || pair_tiles * 6 <= sms) return f8::launch_rows<128, 2, 2>(p, a, w, dev, st);
+    // Pairs from 129 rows on, unless their 256 x 256 tiles (no K split) would be so few
+    // that the row form can give each tile of 128 x 128 two SMs, which split K.  At
+    // K = 4096, by rows and by pairs: 256 x 4608 14.2 and 19.6 us, 1024 x 1152 14.0 and
+    // 19.7, 8192 x 128 15.3 and 19.6; without a split 256 x 5120 21.1 and 19.8, 1024 x
+    // 1280 20.8 and 19.7, 512 x 6144 39.3 and 21.0.  (K <= 256: within 0.7 us.)
+    const int weight_tiles = sms / 2 / ((M + 127) / 128);
+    if (M <= 128 || (int64_t)weight_tiles * 128 >= N) return f8::launch_rows<128, 2, 2>(p, a, w, dev, st);
     return f8::launch_pair(p, a, w, dev, sms, st);
 }

@@ -12,7 +12,8 @@ import pytest
 import torch
 
 from lossless_diffusion_speculative_b200 import binding as ob
-from test_gpu_layer_ops import TYPES, close, gen, half_step, paged_cache, paged_ref, randn, run_paged, tiny
+from test_gpu_layer_ops import (TYPES, check_product, close, fp8_operands, gen, guard, half_step, paged_cache, paged_ref, randn,
+                                run_paged, tiny)
 
 pytestmark = pytest.mark.gpu
 
@@ -219,3 +220,18 @@ def test_rope_sines_and_cosines_to_the_last_bits(rot, D, layout):
     for at, want in ((ia, ang.cos()), (ib, ang.sin())):
         # (a step of fp32 is at most 2^-23 of the value; the angle's second order, 64 bits)
         close(out[:, 0, at], want, 2.5 * 2.0 ** -23 * want.abs() + 1e-13, "turn")
+
+
+# --------------------------------------------------------------------- product
+@pytest.mark.parametrize("M,N,K", [(256, 4608, 400), (129, 4609, 400), (256, 5120, 400), (512, 2304, 400), (513, 1536, 400),
+                                   (1024, 1152, 144), (1025, 1152, 144), (1025, 700, 272),
+                                   (9472, 128, 144), (9473, 128, 144)])
+@pytest.mark.parametrize("out", list(TYPES))
+def test_fp8_matmul_where_its_forms_meet(M, N, K, out):
+    """Sizes on both sides of the change from the row form to the pairs."""
+    g = gen(M + N + K)
+    a, sa, w, sw = fp8_operands(g, M, N, K)
+    o, ok = guard(M, N, dtype=TYPES[out])
+    ob.orthrus_fp8_matmul(a, sa, w, sw, o)
+    check_product(o, a, sa, w, sw)
+    assert ok()
