@@ -235,3 +235,61 @@ def test_fp8_matmul_where_its_forms_meet(M, N, K, out):
     ob.orthrus_fp8_matmul(a, sa, w, sw, o)
     check_product(o, a, sa, w, sw)
     assert ok()
+
+
+# ------------------------------------------------------- sums, streams, layers
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H", [(300, 32767), (2, 32766), (301, 16384), (301, 9999), (40000, 3), (5, 32768)])
+def test_rmsnorm_sums_of_the_widest_rows(dtype, T, H):
+    """x + residual: one fp32 addition (exact for 16-bit values but for the last
+    bits, 2^-24), rounded once."""
+    dt, g = TYPES[dtype], gen(T + H)
+    x, w, r = randn(g, T, H).to(dt), (1 + 0.3 * randn(g, H)).to(dt), randn(g, T, H).to(dt)
+    out = torch.empty_like(x)
+    so, ok = guard(T, H, dtype=dt)
+    ob.orthrus_rmsnorm(x, w, 1e-5, out=out, residual=r, sum_out=so)
+    s = x.double() + r.double()
+    close(so, s, (half_step(dt) + 2.0 ** -23) * s.abs() + tiny(dt), "sum")
+    assert ok()
+
+
+def test_operators_of_two_streams_at_once():
+    """A norm to 8 bits, a product of each form, a rotation and attention on each of
+    two streams, interleaved: bitwise what they give alone."""
+    g = gen(89)
+    turns = ob.orthrus_rope_table(128, 1e6)[0].cuda()
+    jobs = []
+    for T, M, N in ((700, 600, 1536), (33, 20, 3000)):
+        K, B, Hq, Hkv, D = 512, 5, 8, 2, 128
+        a, sa, w, sw = fp8_operands(g, M, N, K)
+        x, wn, r = randn(g, T, 1536).bfloat16(), randn(g, 1536).bfloat16(), randn(g, T, 1536).bfloat16()
+        q, pos = randn(g, T, Hq, D).bfloat16(), torch.arange(T, dtype=torch.int32, device="cuda")
+        lens = [3000, 17, 0, 400, 9001]
+        kp, vp, table = paged_cache(g, lens, 16, Hkv, D, torch.bfloat16)
+        aq, ctx = randn(g, B, Hq, D).bfloat16(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+        ws = torch.zeros(ob.orthrus_paged_attn_workspace_size(B, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+        outs = [torch.empty_like(x), torch.empty_like(x, dtype=torch.float8_e4m3fn), torch.empty(T, 12, device="cuda"),
+                torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty_like(q), torch.empty_like(aq)]
+
+        def run(stream, a=a, sa=sa, w=w, sw=sw, x=x, wn=wn, r=r, q=q, pos=pos, kp=kp, vp=vp, table=table, aq=aq, ctx=ctx,
+                ws=ws, outs=outs):
+            so, q8, s8, o, qo, ao = outs
+            ob.orthrus_rmsnorm(x, wn, 1e-6, residual=r, sum_out=so, out_fp8=q8, out_scale=s8, stream=stream)
+            ob.orthrus_fp8_matmul(a, sa, w, sw, o, stream=stream)
+            ob.orthrus_rope(q, None, pos, turns, qo, stream=stream)
+            ob.orthrus_paged_attn(aq, kp, vp, table, ctx, ao, ws, stream=stream)
+
+        run(None)
+        torch.cuda.synchronize()
+        jobs.append((run, outs, [t.clone() for t in outs]))
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for run, outs, _ in jobs:
+        for t in outs:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for (run, _, _), side in zip(jobs, sides):
+            run(side)
+    torch.cuda.synchronize()
+    for _, outs, want in jobs:
+        assert all(torch.equal(t.view(torch.uint8), w.view(torch.uint8)) for t, w in zip(outs, want))
