@@ -347,15 +347,24 @@ __global__ void __launch_bounds__(MAXT) norm_any_kernel(const NormArgs p)
     if (!NORM || p.out_fp8) {
         uint8_t *o = p.out_fp8 + row * H;
         float *os = p.out_scale + row * ((H + 127) / 128);
+        // one lane makes each group's scale (chunk c has two groups), and every lane
+        // takes all of them: a scale costs as much as five exchanges
+        float mine = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * NC; ++i) {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(s[i / 2][4 * (i & 1) + j]));
+            m = lanes_max(m, 16);
+            if (lane == i) mine = m;
+        }
+        const Scale own = scale_of(mine);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int g0 = ((c * W + wr) * 256) >> 7;               // first of the chunk's two groups
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float m = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(s[c][4 * h + j]));
-                Scale sc = scale_of(lanes_max(m, 16));
+                Scale sc = {__shfl_sync(~0u, own.s, 2 * c + h), __shfl_sync(~0u, own.inv, 2 * c + h)};
                 const float scale = sc.s;
                 if (!live) continue;
                 if (sc.inv == 0.f) {
@@ -400,7 +409,7 @@ template <typename T, int NC, bool NORM> cudaError_t launch_norm(const NormArgs 
                : vec == 2 ? go(std::integral_constant<int, 2>{})
                           : go(std::integral_constant<int, 1>{});
     }
-    const int64_t resident = (int64_t)sms * (warps > 8 ? 1 : NORM ? 2 : 5);
+    const int64_t resident = (int64_t)sms * (warps > 8 ? 1 : NORM ? 2 : NC < 4 ? 5 : sizeof(T) == 2 ? 3 : 2);
     const dim3 grid((unsigned)(blocks < resident ? blocks : resident));
     if constexpr (NORM) {
         if (warps > 16) return launch_pdl(norm_rows_kernel<T, NC, NORM, 1024>, grid, warps * 32, 0, st, a);
@@ -416,12 +425,16 @@ template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, int vec,
     // (more loads in flight, fewer partial sums).
     const int chunks = (a.H + 255) / 256;
     // (The element path holds no loads back and takes as few as keep a row within
-    // eight warps: 92 -> 58 us at 4000 x 4597.  Without the norm two chunks and five
-    // blocks per SM do better than four and three: 51 against 57 us at 8192 x 12288.)
+    // eight warps.  Without the norm four chunks share a scale's cost, but have fewer
+    // warps: from three rounds of them on, and where no lane goes empty; two and four
+    // chunks take 58 and 54 us at 8192 x 12288, 31.6 and 27.5 at 8192 x 4096 fp32, but
+    // 15.8 and 16.9 at 16384 x 1536, 4.1 and 4.6 at 400 x 12288, and 17.8 and 24.7 on
+    // the element path at 4000 x 4596.)
     int nc = a.T <= 2 * sms ? 1
              : vec < 8      ? (chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4)
                             : (chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1);
-    if (!NORM && nc > 2) nc = 2;
+    const bool four = vec == 8 && (chunks % 4 == 0 || chunks > 16) && (int64_t)a.T * chunks >= 3ll * 96 * sms;
+    if (!NORM && nc > 2 && !four) nc = 2;
     while (NORM && nc < 4 && nc * 32 < chunks) nc *= 2;
     a.W = (chunks + nc - 1) / nc;
     if (NORM) {                                  // a block holds whole rows

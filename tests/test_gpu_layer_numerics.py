@@ -82,6 +82,29 @@ def test_quantize_values_over_the_exponent_range(e, width):
     check_values(q, plain_values(x, sc))
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,H", [(3000, 4096), (2200, 5000), (1500, 8200), (6000, 1536), (45000, 1024)])
+@pytest.mark.parametrize("e", [0, -14])
+def test_quantize_values_of_many_rows(dtype, T, H, e):
+    """Rows enough for four chunks a lane (and, at 1536 columns, two), with groups
+    of zeros, and a NaN and an infinity in groups of their own."""
+    g = gen(T + H)
+    x = torch.ldexp(randn(g, T, H), torch.tensor(e, device="cuda")).to(TYPES[dtype])
+    x[T // 2, :256] = 0
+    x[T - 1, H - 1], x[T - 2, 3] = math.nan, math.inf
+    q, sc = quantized(x)
+    plain = x.float()
+    plain[T - 1, H - 1] = 0                                # (a NaN does not enter the maximum)
+    assert torch.equal(sc, plain_scales(plain))
+    assert q[T - 1, H - 1].float().isnan() and q[T - 2, 3].float().isnan() and int(q.float().isnan().sum()) == 2
+    assert (q[T - 2, 4:128].float() == 0).all()
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[T - 2] = False
+    plain[T - 2, 3] = 0
+    q[T - 1, H - 1] = 0
+    check_values(q[keep], plain_values(plain, sc)[keep])
+
+
 def borders(seed, groups, e):
     """[groups, 128]: values on and up to two steps beside the borders between
     neighbouring e4m3 values (of each significand, below 2^-6 as well), times
