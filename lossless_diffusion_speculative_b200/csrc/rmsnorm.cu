@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(MAXT) norm_rows_kernel(const NormArgs p)
 // ---- element path: rows that are not 16-byte aligned, or whose width is not a
 // multiple of 8.  The same parts of a row; a lane's 8 values of a chunk are V at
 // a time, strips of 32 V columns: four values, pairs or single ones, as every
-// row is aligned for them (1113 x 10780 with four 31 us, with pairs 44).
+// row is aligned for them (1113 x 10780 with residual to 8 bits, with four 39 us, with pairs 50).
 template <typename T, int V> union Few {
     using Raw = std::conditional_t<sizeof(T) * V == 2, uint16_t,
                                    std::conditional_t<sizeof(T) * V == 4, uint32_t,
@@ -424,14 +424,16 @@ template <typename T, bool NORM> cudaError_t launch_norm_v(NormArgs &a, int vec,
     // warps as it has chunks (latency); many rows give a lane up to four chunks
     // (more loads in flight, fewer partial sums).
     const int chunks = (a.H + 255) / 256;
-    // (The element path holds no loads back and takes as few as keep a row within
-    // eight warps.  Without the norm four chunks share a scale's cost, but have fewer
+    // The element path holds no loads back: one chunk up to eight warps, then two.
+    // 4000 rows with residual to 8 bits take with one and two 45 and 37 us at 4095
+    // columns, with two and four 71 and 76 at 4597, 75 and 111 at 4598, 65 and 97 at
+    // 8188.  Without the norm four chunks share a scale's cost, but have fewer
     // warps: from three rounds of them on, and where no lane goes empty; two and four
-    // chunks take 58 and 54 us at 8192 x 12288, 31.6 and 27.5 at 8192 x 4096 fp32, but
-    // 15.8 and 16.9 at 16384 x 1536, 4.1 and 4.6 at 400 x 12288, and 17.8 and 24.7 on
-    // the element path at 4000 x 4596.)
+    // take 58 and 54 us at 8192 x 12288, 31.6 and 27.5 at 8192 x 4096 fp32, but 15.8
+    // and 16.9 at 16384 x 1536, 4.1 and 4.6 at 400 x 12288, and 17.8 and 24.7 on the
+    // element path at 4000 x 4596.
     int nc = a.T <= 2 * sms ? 1
-             : vec < 8      ? (chunks <= 8 ? 1 : chunks <= 16 ? 2 : 4)
+             : vec < 8      ? (chunks <= 8 ? 1 : chunks <= 32 ? 2 : 4)
                             : (chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1);
     const bool four = vec == 8 && (chunks % 4 == 0 || chunks > 16) && (int64_t)a.T * chunks >= 3ll * 96 * sms;
     if (!NORM && nc > 2 && !four) nc = 2;
