@@ -483,9 +483,11 @@ ORTHRUS_API int orthrus_qkv_project(const void *x, const void *w_q, const void *
  *             (the scale as the fp32 product with the nearest value to 1 / 448;
  *             the nearest fp32 quotient, rounded to the nearest e4m3 value), so
  *             value * scale stands for y and a group of zeros has a finite scale.
- *             A NaN stays a NaN and does not enter the maximum.
+ *             A NaN stays a NaN and does not enter the maximum; in a group with an
+ *             infinity the scale is infinite, finite values are 0 and infinite NaN.
  *             At least one of out and out_fp8 is given.
- * Supported: H <= ORTHRUS_MAX_NORM_WIDTH, any T.  16-byte aligned pointers,
+ * Supported: 1 <= H <= ORTHRUS_MAX_NORM_WIDTH, 1 <= T < 2^26 (an empty batch is an
+ * ORTHRUS_ERR_ARG, as in every call here).  16-byte aligned pointers,
  * x_stride and H multiples of 8 take the vector path; anything else is read
  * four, two or one values at a time, as its alignment allows.
  */
@@ -509,7 +511,8 @@ ORTHRUS_API int orthrus_quantize_fp8(orthrus_dtype dtype, const void *x, int64_t
  *     out[m, n] = sum_kb a_scale[m, kb] * w_scale[n / 128, kb] *
  *                 sum_{k in block kb} a[m, k] * w[n, k]
  * fp32 throughout (the products of a block are summed on the tensor cores,
- * each block's sum is scaled and added in fp32), rounded once to out_dtype.
+ * each block's sum is multiplied by the fp32 product of its two scales and added
+ * in fp32), rounded once to out_dtype.
  *
  *   a        [M, K] e4m3, dense;  a_scale [M, ceil(K / 128)] fp32.
  *   w        [N, K] e4m3, dense;  w_scale [ceil(N / 128), ceil(K / 128)] fp32
@@ -644,7 +647,7 @@ ORTHRUS_API int orthrus_rope_append(orthrus_dtype dtype, orthrus_rope_layout lay
  *             types may share a workspace that is large enough for each, one
  *             after another; calls that overlap on the device must not.
  * Supported: D 64, 128 or 256; Hq % Hkv == 0; B <= 4096; any page_size.  q, the
- * pages and the workspace 16-byte aligned.
+ * pages, out and the workspace 16-byte aligned.
  * Numerics: products of 16-bit values are exact in fp32; the softmax weights
  * enter the second product as three bf16 terms (24 bits) or two fp16 ones (22
  * bits, and 2^-32 of the largest weight), the statistics are fp32, the

@@ -40,37 +40,7 @@ template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// Eight consecutive values at a 16-byte aligned address.
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[8])
-{
-    if constexpr (sizeof(T) == 2) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2<T>(u[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    } else {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
-}
-
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8])
-{
-    if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4 *>(p) =
-            make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-    } else {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-}
-
-// Eight consecutive values as loaded (not yet converted), so that loads can be
+// Eight consecutive values at a 16-byte aligned address, as loaded (not yet converted), so that loads can be
 // in flight without holding fp32 registers.
 template <typename T> struct Raw8 {
     uint4 w[sizeof(T) / 2];

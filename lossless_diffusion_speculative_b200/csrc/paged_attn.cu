@@ -9,8 +9,8 @@
 // board's power: under a sustained load that reaches the power limit the clocks,
 // and the memory rate with them, fall (by 11 % for twice the matrix
 // instructions).  Measured, 8 KV heads of 128: 8 long sequences of 273,000 keys in
-// all 170 us (6.6 TB/s, a copy's rate; 178 at the power limit), 16 ragged ones of
-// 154,000 104 us (93 %), one of 300 keys 8.1.  G <= 16 rows would fill an eighth of
+// all 170 us (6.6 TB/s, a copy's rate; 178 to 186 at the power limit), 16 ragged ones
+// of 154,000 103 us (94 %), one of 300 keys 7.7.  G <= 16 rows would fill an eighth of
 // a tcgen05 tile's 128 and pay its TMEM round trips per tile, so the products run
 // on mma.sync m16n8k16, transposed: 16 keys (then 16 dims) are the instruction's rows and 8 heads its
 // columns, so that up to 8 heads waste nothing.  The weights go from the first
@@ -203,7 +203,7 @@ __device__ __forceinline__ void join_statistics(const Args &p, int rows, int n, 
 // rows with the loads of four partials in flight (a segment of one sequence can
 // have a partial from every block of the grid).  With pieces enough each of the
 // four warps has its own (2 sequences of 16,000, 8 heads of 128, 16 rows each:
-// 35.6 -> 33.9 us);
+// 36.6 -> 34.8 us);
 // else every warp takes every fourth partial, and the four sums are added in order
 // through shared memory (`area(w)`: 2 KB of warp w).  All threads of the block.
 template <typename T, int D, class S, class A>

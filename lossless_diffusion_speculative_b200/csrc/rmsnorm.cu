@@ -11,8 +11,10 @@
 // group lies within one warp's chunk of 256 columns: 16 lanes of 8 consecutive
 // values on the vector path, or strips of 32 lanes where rows are not 16-byte
 // aligned, so its maximum needs shuffles only.  HBM-bound, measured: 16384 x 4096 bf16 with
-// residual to 8 bits 76 us (6.2 TB/s, 94 % of a copy's rate), 8192 x 12288
-// quantised 49 us (96 %) in short runs and 54 where the power limit holds.
+// residual to 8 bits 73 us (6.4 TB/s, 98 % of a copy's rate) in short runs and 79-82
+// where the power limit holds, 8192 x 12288 quantised 50 us (94 %) and 54-56.
+// (The 1024-thread instances, 64 registers a thread, keep part of two and four
+// chunks a lane in local memory: 2000 x 32768 with residual to 8 bits 181 us, floor 70.)
 #include <math.h>
 
 #include <type_traits>
