@@ -258,7 +258,9 @@ ORTHRUS_API size_t orthrus_rejection_workspace_size(int B, int K, int V);
  *                aligned.  Zero-fill it once before its first use: its leading
  *                per-sequence counters must be zero when a call starts, and
  *                every call leaves them zero again (the rest is clobbered).
- *                Calls that overlap on the device must not share it.
+ *                Where the counters lie depends on B: zero-fill it again before
+ *                a call with another B.  Calls that overlap on the device must
+ *                not share it.
  * Supported: K <= ORTHRUS_MAX_BLOCK, V <= 262144, B * K <= 65535.
  * Numerics: fp32 with exp2 on the special-function unit; a decision whose
  * margin is within ~1e-6 relative of its threshold can differ from an exact
@@ -439,7 +441,9 @@ ORTHRUS_API int orthrus_lm_head_consensus(const void *hidden, const void *lm_hea
  *   workspace    >= orthrus_qkv_workspace_size() bytes, 16-byte aligned,
  *                zero-filled once before first use (its per-tile counters must
  *                be zero when a call starts; every completed call leaves them
- *                zero).  Calls that overlap on the device must not share it.
+ *                zero).  Where the counters lie depends on the shape: zero-fill
+ *                it again before a call of another shape.  Calls that overlap on
+ *                the device must not share it.
  * Supported: B * K <= ORTHRUS_MAX_LM_ROWS, hidden a multiple of 64, D a
  * multiple of 16, Hq % Hkv == 0; x, the weights and the workspace 16-byte
  * aligned; sm_100 devices only.
